@@ -133,8 +133,8 @@ def _tree(case):
 
 def _pack(parent, lens):
     """The depth-first packing (children by ascending id): per token, the token before it on its root path (-1 before a
-    root) and its depth; per node, the token that its final state belongs to (-1: none) and the first token of each node
-    that starts from nothing."""
+    root) and its depth; per node, its last token (-1: it has none); the nodes that start from nothing, each with its first
+    token."""
     m = len(parent)
     kids = [[] for _ in range(m)]
     roots = []
@@ -142,20 +142,20 @@ def _pack(parent, lens):
         (roots if parent[v] < 0 else kids[parent[v]]).append(v)
     prev = np.arange(-1, sum(lens) - 1)
     depth = np.zeros(sum(lens), np.int64)
-    last, base, starts, at = [-1] * m, [0] * m, [], 0
+    last, state, base, starts, at = [-1] * m, [-1] * m, [0] * m, [], 0
     stack = roots[::-1]
     while stack:
         v = stack.pop()
-        above = last[parent[v]] if parent[v] >= 0 else -1
+        above = state[parent[v]] if parent[v] >= 0 else -1
         base[v] = base[parent[v]] + lens[parent[v]] if parent[v] >= 0 else 0
-        last[v] = above
+        state[v] = above
         if lens[v]:
             prev[at] = above
             if above < 0:
                 starts.append((v, at))
             depth[at:at + lens[v]] = base[v] + np.arange(lens[v])
             at += lens[v]
-            last[v] = at - 1
+            last[v] = state[v] = at - 1
         stack.extend(kids[v][::-1])
     return prev, depth, np.array(last), starts
 
@@ -272,9 +272,7 @@ def _plain_scan(s):
         b = b + A * b[at]
         A = A * A[at]
     h = b[:n]
-    final = torch.cat([h, one])[s["last"]]
-    if case["init"]:
-        final = torch.where((s["last"] < 0)[:, None], s["init"], final)
+    final = torch.cat([h, one])[s["last"]]  # zeros for nodes without tokens: -1 is the row of zeros
     out = dict(y=h.to(s["x"].dtype), final=final)
     if not case["train"]:
         return out
@@ -289,7 +287,7 @@ def _plain_scan(s):
     before = b[s["jumps"][0][:n]] if s["jumps"] else torch.zeros_like(h)
     if case["init"]:
         before[s["root_tokens"]] = s["init"][s["root_nodes"]]
-        d_init = torch.where((s["last"] < 0)[:, None], s["d_final"], 0.0)
+        d_init = torch.zeros_like(s["init"])
         d_init[s["root_nodes"]] = a[s["root_tokens"]] * lam[s["root_tokens"]]
         out["d_init"] = d_init
     if weight is None:
@@ -456,21 +454,18 @@ def _exact_scan(s):
         h[rows] = a[rows] * before[rows] + b[rows]
     lt = torch.from_numpy(np.where(last < 0, n, last)).to(dev)
     final = h[lt]
-    if case["init"]:
-        none = torch.from_numpy(last < 0).to(dev)
-        final[none] = s["init"].double()[none]
     out = dict(y=h[:n], final=final)
     if not case["train"]:
         return out
     lam = torch.cat([s["dy"].double(), torch.zeros(1, x.shape[1], dtype=torch.float64, device=dev)])
     if case["init"]:
-        lam.index_add_(0, lt, s["d_final"].double())
+        lam.index_add_(0, lt, s["d_final"].double())  # row n takes those of nodes without tokens
     for i in range(len(cuts) - 2, 0, -1):
         rows, above = order_t[cuts[i]:cuts[i + 1]], up[cuts[i]:cuts[i + 1]]
         lam.index_add_(0, above, a[rows] * lam[rows])
     lam = lam[:n]
     if case["init"]:
-        d_init = torch.where(torch.from_numpy(last < 0).to(dev)[:, None], s["d_final"].double(), 0.0)
+        d_init = torch.zeros_like(s["init"], dtype=torch.float64)
         for v, t in starts:
             d_init[v] = a[t] * lam[t]
         out["d_init"] = d_init
