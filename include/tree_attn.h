@@ -168,6 +168,31 @@ int tree_rope_fwd(const tree_plan_t* plan, const tree_bf16* q, const tree_bf16* 
 int tree_apply_weights(const tree_plan_t* plan, const tree_bf16* u, tree_bf16* dO, int H,
                        int d, tree_stream_t stream);
 
+#define TREE_MAX_AXES 4
+
+/* Rotary positions with several axes, for trees that hold image or video patches next to text: a
+ * patch has a position on each axis (say time, height, width), a text token the same one on all.
+ * pos: device int32 [n_axes][N], the tokens' positions in packed order (any int32, also
+ * negative).  Frequency c < d/2 turns by pos[axis(c)] * theta^(-2c/d); sections (host int32
+ * [n_axes], sum d/2, each >= 0) say how many frequencies an axis has: interleaved = 0, the first
+ * sections[0] are axis 0's, the next sections[1] axis 1's, and so on; interleaved = 1, axis i >= 1
+ * has i, i + n_axes, i + 2 n_axes, ... until it has its share (all of them below d/2), and axis 0
+ * what is left.  Rotate-half pairs and layouts as tree_rope_fwd; in place allowed.  The angle is
+ * exact to 2^-24 turns at every position.  One axis with pos = the plan's `pos` is
+ * tree_rope_fwd with more exact angles.  n_axes outside 1..TREE_MAX_AXES, sections that do not
+ * describe d/2 frequencies, d not 64/128, bad heads or theta -> TREE_ERR_SHAPE. */
+int tree_rope_axes_fwd(const tree_plan_t* plan, const int32_t* pos, const int32_t* sections,
+                       int n_axes, int interleaved, const tree_bf16* q, const tree_bf16* k,
+                       tree_bf16* qr, tree_bf16* kr, int Hq, int Hkv, int d, float theta,
+                       tree_stream_t stream);
+
+/* Its backward: the gradients w.r.t. the rotated q and k (tree_attn_bwd with rope_theta <= 0) are
+ * rotated back to gradients w.r.t. q and k.  Arguments as the forward's; in place allowed. */
+int tree_rope_axes_bwd(const tree_plan_t* plan, const int32_t* pos, const int32_t* sections,
+                       int n_axes, int interleaved, const tree_bf16* dqr, const tree_bf16* dkr,
+                       tree_bf16* dq, tree_bf16* dk, int Hq, int Hkv, int d, float theta,
+                       tree_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * Attention (section 4.2: Softmax(Q K^T / sqrt(d) + M) V, block-sparse per section 4.3)
  * -------------------------------------------------------------------------------------*/
@@ -335,6 +360,48 @@ int tree_route_states(const int32_t* parent, const int32_t* node_len, int32_t n_
 int tree_route_states_bwd(const int32_t* parent, const int32_t* node_len, int32_t n_nodes,
                           const float* d_init, int S, float* d_final, tree_stream_t stream);
 
+/* Element types of the entry points that take more than bf16. */
+enum { TREE_BF16 = 0, TREE_F32 = 1 };
+
+/* Gates of tree_scan_fwd: how gate values g become the decay a and the input b.
+ *   TREE_GATE_SIGMOID: a = sigmoid(g), b = (1 - a) x
+ *   TREE_GATE_LOG:     a = exp(min(g, 0)), b = x   (g a log decay; no gradient where g > 0) */
+enum { TREE_GATE_SIGMOID = 0, TREE_GATE_LOG = 1 };
+
+/* Bytes of workspace tree_scan_fwd and tree_scan_bwd need for C channels. */
+size_t tree_scan_workspace(const tree_plan_t* plan, int C);
+
+/* Gated linear recurrence along root paths (section 9.1, the layer whose states tree_route_states
+ * hands over, with the hand-over inside):
+ *   h_t = a_t h_prev(t) + b_t,  y_t = h_t  per channel,
+ * prev(t) the token before t on its root path (as in tree_conv1d_fwd).  A node with no
+ * token-holding ancestor starts from its row of init (fp32 [n_nodes][C], other rows are not read),
+ * or from zero if init is NULL.  One-token nodes without parents are a decoding step.
+ * gate, x, y: [N][C] in packed order, all of type dtype (TREE_BF16 or TREE_F32).
+ * states: fp32 [n_nodes + n_tiles][C].  Row v < n_nodes receives node v's final state (zeros where
+ * the node holds no tokens), row n_nodes + k the state after the last token of tile k: what the
+ * backward starts from.  States are fp32 throughout; y is rounded once.  A state that becomes
+ * infinite or NaN stays so (either) along its paths and touches no other path.
+ * C a multiple of 8 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
+ * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at
+ * a time.  Deterministic.  status_dev (device int32, may be NULL) as for tree_attn_fwd. */
+int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len,
+                  const void* gate, const void* x, const float* init, int C, int dtype,
+                  int gate_kind, void* workspace, void* y, float* states, int32_t* status_dev,
+                  tree_stream_t stream);
+
+/* Backward of tree_scan_fwd for the upstream gradient dy [N][C] (type dtype) and, if d_final is not
+ * NULL, that of the final states (fp32 [n_nodes][C]; rows of nodes without tokens are not read).
+ * gate, x, init, states: the forward's.  Writes dgate, dx [N][C] (type dtype) and, if d_init is not
+ * NULL, the gradient of init (fp32 [n_nodes][C], zeros in rows that the forward does not read).
+ * h is computed again from states.  Deterministic: a node's state collects its children's gradients
+ * from the last child to the first.  Rules as tree_scan_fwd. */
+int tree_scan_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len,
+                  const void* gate, const void* x, const float* init, const float* states,
+                  const void* dy, const float* d_final, int C, int dtype, int gate_kind,
+                  void* workspace, void* dgate, void* dx, float* d_init, int32_t* status_dev,
+                  tree_stream_t stream);
+
 /* ---------------------------------------------------------------------------------------
  * Loss: the tree's next-token cross-entropy fused with the vocabulary projection
  * ("Tree Training 技术详解", sections 6.2, 6.3 and 12).  Each root-to-leaf path is a sequence
@@ -363,6 +430,37 @@ int tree_ce_fwd_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_
                     const tree_bf16* h, const tree_bf16* W, const int32_t* labels, int D, int V,
                     int chunk, int ignore_index, void* workspace, float* loss, float* lse,
                     tree_bf16* dh, float* dW, int32_t* status_dev, tree_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Gradients of a step: the norm over all of them, and clipping
+ * -------------------------------------------------------------------------------------*/
+
+/* One gradient of a step: numel contiguous elements of type dtype (TREE_BF16 or TREE_F32), aligned to
+ * their type.  out: where tree_grad_clip writes them (the same type; grad itself for in place). */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t numel; /* >= 0 */
+  int32_t dtype;
+  int32_t reserved;
+} tree_grad_t;
+
+/* Bytes of workspace (16-byte aligned, not initialised) for a list of n gradients. */
+size_t tree_grad_workspace(int n);
+
+/* *norm (device fp32) = sqrt of the sum of squares of every element of the n >= 1 gradients (the
+ * list is host memory, free when the call returns).  Summed in fp64; the norm is right wherever it
+ * is an fp32 number, also where the squares are not.  Infinite or NaN elements give such a norm.
+ * Deterministic. */
+int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
+                   tree_stream_t stream);
+
+/* The norm as tree_grad_norm, and out = grad * (max_norm / norm) where max_norm < norm, else (also
+ * for an infinite or NaN norm: read it, and skip the step) out = grad.  max_norm >= 0, may be
+ * infinite (else TREE_ERR_SHAPE).  An `out` that overlaps another gradient or `out`, or its own
+ * gradient other than as a whole, is refused (TREE_ERR_ARG), a gradient listed twice in place too. */
+int tree_grad_clip(const tree_grad_t* list, int n, float max_norm, void* workspace, float* norm,
+                   tree_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
  * Diagnostics

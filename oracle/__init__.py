@@ -18,6 +18,8 @@ Modules
                and the associative (max, numerator, denominator) softmax merge.
 ``hybrid``     section 9: the path-expanded causal convolution (forward and backward)
                and the parent-routed recurrent state with its transpose.
+``scan``       section 9.1: the gated linear recurrence along root paths, its gradients, and how
+               far the same in 32 bits may be off.
 ``ce``         sections 6.2, 6.3, 12: the path-averaged next-token cross-entropy with ignore
                labels (loss, logsumexp, gradients of the hidden states and the vocabulary
                matrix), whole and restricted to sampled rows.

@@ -9,11 +9,15 @@ functions carry the C entry points' names (``include/tree_attn.h``):
   tree_apply_weights, tree_attn_fwd, tree_attn_bwd_workspace, tree_attn_bwd,
   tree_attn_fwd_gateway, tree_attn_bwd_gateway, tree_relay_add, tree_gather_rows, tree_conv1d_fwd,
   tree_conv1d_bwd_workspace, tree_conv1d_bwd, tree_route_states, tree_route_states_bwd, tree_ce_workspace,
-  tree_ce_fwd_bwd, tree_selftest_timeout, tree_set_wait_limit_ns (and diag_gemm -> tree_diag_gemm)
+  tree_ce_fwd_bwd, tree_rope_axes_fwd, tree_rope_axes_bwd, tree_scan_workspace, tree_scan_fwd, tree_scan_bwd,
+  tree_grad_norm, tree_grad_clip, tree_selftest_timeout, tree_set_wait_limit_ns (and diag_gemm -> tree_diag_gemm)
 
 Semantics follow "Tree Training 技术详解" (tingdeliu.github.io): DFS packing (section 3.2),
 tree mask (4.2), block table (4.3), depth positions (5), path-count weights (6.2), the
 path-averaged next-token loss (6.2, 6.3, 12), hybrid layers (9).
+
+Host bookkeeping next to the kernels: tree_axis_positions (positions of a tree with image patches),
+tree_grad_list (a step's gradients, gathered once).
 """
 from __future__ import annotations
 
@@ -65,6 +69,10 @@ class PlanT(ctypes.Structure):
                                                       ("n_tiles", _i32), ("n_paths", _i32)]
 
 
+class GradT(ctypes.Structure):
+    _fields_ = [("grad", _vp), ("out", _vp), ("numel", _i64), ("dtype", _i32), ("reserved", _i32)]
+
+
 class Gateway(ctypes.Structure):
     _fields_ = [("k", _vp), ("v", _vp), ("len", _i32)]
 
@@ -107,6 +115,17 @@ def _lib():
         "tree_conv1d_bwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp]),
         "tree_route_states": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _vp]),
         "tree_route_states_bwd": (_i32, [_vp, _vp, _i32, _vp, _i32, _vp, _vp]),
+        "tree_rope_axes_fwd": (_i32, [P(PlanT), _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32,
+                                      _vp]),
+        "tree_rope_axes_bwd": (_i32, [P(PlanT), _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32,
+                                      _vp]),
+        "tree_scan_workspace": (ctypes.c_size_t, [P(PlanT), _i32]),
+        "tree_scan_fwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
+        "tree_scan_bwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                 _vp, _vp, _vp]),
+        "tree_grad_workspace": (ctypes.c_size_t, [_i32]),
+        "tree_grad_norm": (_i32, [_vp, _i32, _vp, _vp, _vp]),
+        "tree_grad_clip": (_i32, [_vp, _i32, _f32, _vp, _vp, _vp]),
         "tree_ce_workspace": (ctypes.c_size_t, [P(PlanT), _i32, _i32, _i32]),
         "tree_ce_fwd_bwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _vp]),
@@ -552,3 +571,228 @@ def diag_gemm(A, B, M, N, K, a_mn, b_mn, status=None, stream=None):
     _check(_lib().tree_diag_gemm(_ptr(A), _ptr(B), M, N, K, int(a_mn), int(b_mn), _ptr(C), _ptr(status),
                                  _stream(stream)), "tree_diag_gemm")
     return C
+
+
+class _Launch:
+    """Makes `device` the current one and `stream` (default: the device's current one) the current stream, so
+    that what a call allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, device, stream):
+        self.device = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream = None if stream is None else torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.device is not None:
+            self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        if self.stream is not None:
+            self.stream.__exit__(*exc)
+        if self.device is not None:
+            self.device.__exit__(*exc)
+
+
+def _need_on(device, t, shape, dtype, name):
+    """_need, and on the plan's device."""
+    _need(t, shape, dtype, name)
+    if t.device != device:
+        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+
+
+def _rope_axes(name, plan, pos, q, k, sections, theta, interleaved, oq, ok, stream):
+    Hq, Hkv, d = _heads(plan, q, k)
+    dev, n_axes = plan.device, len(sections)
+    for t, what in ((q, "q"), (k, "k")):
+        _need_on(dev, t, tuple(t.shape), torch.bfloat16, what)
+    _need_on(dev, pos, (n_axes, plan.n_tokens), torch.int32, "pos")
+    for t, like, what in ((oq, q, "the q output"), (ok, k, "the k output")):
+        if t is not None:
+            _need_on(dev, t, tuple(like.shape), torch.bfloat16, what)
+    sec = (_i32 * max(1, n_axes))(*[int(s) for s in sections])
+    with _Launch(dev, stream) as st:
+        oq = torch.empty_like(q) if oq is None else oq
+        ok = torch.empty_like(k) if ok is None else ok
+        _check(getattr(_lib(), name)(plan.ref(), _ptr(pos), sec, n_axes, int(bool(interleaved)), _ptr(q), _ptr(k),
+                                     _ptr(oq), _ptr(ok), Hq, Hkv, d, float(theta), st), name)
+    return oq, ok
+
+
+def tree_rope_axes_fwd(plan: TreePlan, pos, q, k, sections, theta=10000.0, interleaved=False, qr=None, kr=None,
+                       stream=None):
+    """Rotate-half RoPE with several axes: pos [n_axes, N] int32, sections the frequencies of each axis (sum
+    d/2), in runs or interleaved.  Returns (qr, kr); pass qr=q, kr=k for in place."""
+    return _rope_axes("tree_rope_axes_fwd", plan, pos, q, k, sections, theta, interleaved, qr, kr, stream)
+
+
+def tree_rope_axes_bwd(plan: TreePlan, pos, dqr, dkr, sections, theta=10000.0, interleaved=False, dq=None, dk=None,
+                       stream=None):
+    """Its backward: gradients w.r.t. the rotated q and k (tree_attn_bwd with rope_theta=0) rotated back.
+    Returns (dq, dk); in place allowed."""
+    return _rope_axes("tree_rope_axes_bwd", plan, pos, dqr, dkr, sections, theta, interleaved, dq, dk, stream)
+
+
+def tree_axis_positions(parent, node_len, extent, local, base=0):
+    """Positions for tree_rope_axes_fwd on a tree, on the host: int32 [n_axes, N] in packed order.  local
+    [n_axes, N]: each token's position within its node (a text token's offset on every axis, an image patch's
+    time, row and column); extent [n_nodes]: how far a node moves the positions behind it on (its token
+    count for text, the largest side for an image).  A token's position is base + the extents of its node's
+    ancestors + its local one."""
+    nodes = tree_plan_nodes(parent, node_len)
+    par, nl = _host_i32(parent), _host_i32(node_len)
+    extent, local = np.asarray(extent, dtype=np.int64), np.asarray(local, dtype=np.int64)
+    if extent.shape != par.shape:
+        raise ValueError("extent and parent differ in length")
+    if local.ndim != 2 or local.shape[1] != int(nl.sum(dtype=np.int64)):
+        raise ValueError("local must be [n_axes, N]")
+    start = np.empty(len(par), dtype=np.int64)
+    for v in nodes["order"]:                          # preorder: a parent comes before its children
+        start[v] = base if par[v] < 0 else start[par[v]] + extent[par[v]]
+    out = local + np.repeat(start[nodes["order"]], nl[nodes["order"]])
+    if out.size and (out.min() < -2 ** 31 or out.max() >= 2 ** 31):
+        raise ValueError("positions leave the range of int32")
+    return out.astype(np.int32)
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
+GATES = {"sigmoid": 0, "log": 1}
+
+
+def tree_scan_workspace(plan: TreePlan, C) -> int:
+    """Bytes of workspace tree_scan_fwd and tree_scan_bwd need for C channels."""
+    return int(_lib().tree_scan_workspace(plan.ref(), int(C)))
+
+
+def _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status):
+    parent, node_len = tree
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be [N, C], bf16 or fp32")
+    if gate_kind not in GATES:
+        raise ValueError(f"gate_kind must be one of {sorted(GATES)}")
+    C, dev, n = x.shape[1], plan.device, plan.info.n_nodes
+    _need_on(dev, x, (plan.n_tokens, C), x.dtype, "x")
+    _need_on(dev, gate, (plan.n_tokens, C), x.dtype, "gate")
+    _need_on(dev, parent, (n,), torch.int32, "parent")
+    _need_on(dev, node_len, (n,), torch.int32, "node_len")
+    if init is not None:
+        _need_on(dev, init, (n, C), torch.float32, "init")
+    if status is not None:
+        _need_on(dev, status, (1,), torch.int32, "status")
+    need = tree_scan_workspace(plan, C)
+    if workspace is not None:
+        _need_on(dev, workspace, tuple(workspace.shape), torch.uint8, "workspace")
+        if workspace.numel() < need:
+            raise ValueError(f"workspace: {workspace.numel()} bytes, {need} needed")
+    return C, dev, n, need
+
+
+def tree_scan_fwd(plan: TreePlan, tree, gate, x, init=None, gate_kind="sigmoid", workspace=None, y=None, states=None,
+                  status=None, stream=None):
+    """Gated linear recurrence along root paths: h_t = a_t h_prev(t) + b_t with a = sigmoid(gate), b = (1 - a) x
+    (gate_kind "sigmoid") or a = exp(min(gate, 0)), b = x ("log").  gate, x [N, C] bf16 or fp32; init
+    [n_nodes, C] fp32: the states that nodes without a token-holding ancestor start from.  Returns (y [N, C],
+    states [n_nodes + n_tiles, C] fp32): states[v] is node v's final state, the rest is for tree_scan_bwd."""
+    C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
+    if y is not None:
+        _need_on(dev, y, tuple(x.shape), x.dtype, "y")
+    if states is not None:
+        _need_on(dev, states, (n + plan.n_tiles, C), torch.float32, "states")
+    with _Launch(dev, stream) as st:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        y = torch.empty_like(x) if y is None else y
+        states = torch.empty(n + plan.n_tiles, C, dtype=torch.float32, device=dev) if states is None else states
+        _check(_lib().tree_scan_fwd(plan.ref(), _ptr(tree[0]), _ptr(tree[1]), _ptr(gate), _ptr(x), _ptr(init), C,
+                                    _DTYPES[x.dtype], GATES[gate_kind], _ptr(workspace), _ptr(y), _ptr(states),
+                                    _ptr(status), st), "tree_scan_fwd")
+    return y, states
+
+
+def tree_scan_bwd(plan: TreePlan, tree, gate, x, states, dy, init=None, d_final=None, gate_kind="sigmoid",
+                  workspace=None, dgate=None, dx=None, d_init=None, status=None, stream=None):
+    """Backward of tree_scan_fwd (its gate, x, init and states) for dy [N, C] and d_final [n_nodes, C] fp32, the
+    gradient of the nodes' final states.  Returns (dgate, dx, d_init): d_init [n_nodes, C] fp32 if init or a
+    d_init to write was given, else None."""
+    C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
+    _need_on(dev, dy, tuple(x.shape), x.dtype, "dy")
+    _need_on(dev, states, (n + plan.n_tiles, C), torch.float32, "states")
+    for t, what in ((dgate, "dgate"), (dx, "dx")):
+        if t is not None:
+            _need_on(dev, t, tuple(x.shape), x.dtype, what)
+    for t, what in ((d_final, "d_final"), (d_init, "d_init")):
+        if t is not None:
+            _need_on(dev, t, (n, C), torch.float32, what)
+    with _Launch(dev, stream) as st:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        dgate = torch.empty_like(x) if dgate is None else dgate
+        dx = torch.empty_like(x) if dx is None else dx
+        if d_init is None and init is not None:
+            d_init = torch.empty_like(init)
+        _check(_lib().tree_scan_bwd(plan.ref(), _ptr(tree[0]), _ptr(tree[1]), _ptr(gate), _ptr(x), _ptr(init),
+                                    _ptr(states), _ptr(dy), _ptr(d_final), C, _DTYPES[x.dtype], GATES[gate_kind],
+                                    _ptr(workspace), _ptr(dgate), _ptr(dx), _ptr(d_init), _ptr(status), st),
+               "tree_scan_bwd")
+    return dgate, dx, d_init
+
+
+@dataclass
+class GradList:
+    """A step's gradients gathered for tree_grad_norm and tree_grad_clip (tree_grad_list): the tensors, where
+    clipping writes them, the C list and a workspace.  The tensors' contents are read at every call."""
+    grads: list
+    out: list
+    c: ctypes.Array
+    workspace: torch.Tensor
+    device: torch.device
+
+
+def tree_grad_list(grads, out=None) -> GradList:
+    """Gather contiguous CUDA tensors (bf16 or fp32, any shapes, one device).  out: tensors of the same shapes
+    and types that tree_grad_clip writes; None clips in place.  Gather once and use at every step, for as
+    long as the gradients stay in the same tensors; one call at a time (it holds the workspace)."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("grads is empty")
+    if len(outs) != len(grads):
+        raise ValueError(f"out has {len(outs)} tensors, grads {len(grads)}")
+    dev = grads[0].device
+    c = (GradT * len(grads))()
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if g.dtype not in _DTYPES:
+            raise ValueError(f"grads[{i}]: expected bf16 or fp32, got {g.dtype}")
+        _need_on(dev, g, tuple(g.shape), g.dtype, f"grads[{i}]")
+        if o is not g:
+            _need_on(dev, o, tuple(g.shape), g.dtype, f"out[{i}]")
+        c[i] = GradT(g.data_ptr(), o.data_ptr(), g.numel(), _DTYPES[g.dtype], 0)
+    ws = torch.empty(int(_lib().tree_grad_workspace(len(grads))), dtype=torch.uint8, device=dev)
+    return GradList(grads=grads, out=outs, c=c, workspace=ws, device=dev)
+
+
+def _grad_call(grads, norm, stream, call):
+    gl = grads if isinstance(grads, GradList) else tree_grad_list(grads)
+    if norm is not None:
+        _need_on(gl.device, norm, (1,), torch.float32, "norm")
+    with _Launch(gl.device, stream) as st:
+        norm = torch.empty(1, dtype=torch.float32, device=gl.device) if norm is None else norm
+        call(gl, norm, st)
+    return norm
+
+
+def tree_grad_norm(grads, norm=None, stream=None):
+    """The global norm over a list of tensors or a GradList: fp32 [1], summed in fp64, deterministic."""
+    return _grad_call(grads, norm, stream, lambda gl, nrm, st: _check(
+        _lib().tree_grad_norm(gl.c, len(gl.grads), _ptr(gl.workspace), _ptr(nrm), st), "tree_grad_norm"))
+
+
+def tree_grad_clip(grads, max_norm, norm=None, stream=None):
+    """Scale the gradients by max_norm / norm where their global norm is above max_norm, in place or into the
+    GradList's out; an infinite or NaN norm leaves them as they are.  Returns the norm before, fp32 [1]."""
+    return _grad_call(grads, norm, stream, lambda gl, nrm, st: _check(
+        _lib().tree_grad_clip(gl.c, len(gl.grads), float(max_norm), _ptr(gl.workspace), _ptr(nrm), st),
+        "tree_grad_clip"))
+
+
+__all__ += ["tree_rope_axes_fwd", "tree_rope_axes_bwd", "tree_axis_positions", "tree_scan_workspace",
+            "tree_scan_fwd", "tree_scan_bwd", "GradList", "tree_grad_list", "tree_grad_norm", "tree_grad_clip"]
