@@ -32,8 +32,8 @@ int make_tmap_bf16_2d(CUtensorMap* m, const void* base, int inner, int rows, int
 
 namespace {
 
-constexpr int kScanWarps = 8;               // compute warps; one more warp loads
-constexpr int kScanThreads = 32 * (kScanWarps + 1);
+constexpr int kScanWarps = 8;               // compute warps; one more warp loads, one joins
+constexpr int kScanThreads = 32 * (kScanWarps + 2);
 constexpr int kWarpTokens = TILE / kScanWarps;
 constexpr int kRowBytes = 128;              // a tile's row: 64 bf16 or 32 fp32 channels, a word a lane
 constexpr int kBoxBytes = TILE * kRowBytes;
@@ -41,7 +41,6 @@ constexpr int kScanGroup = 16;              // at most this many maps are joined
 
 constexpr int kLinkChain = -1;             // the token before on the path is the one before in packed order
 constexpr int kLinkRoot = -2;              // the token starts from its node's initial state
-constexpr int kFromTile = 1 << 30;         // mark on a node id (below 2^30): it ends in the tile at hand
 
 struct ScanTree {
   const int32_t* tok_node;
@@ -58,8 +57,9 @@ struct ScanTree {
 //   kid   for a node's last token: the second of the nodes that start from it (the first one is its
 //         successor in packed order), -1 if there is none
 //   sib   for a break: the next node after its own that starts from the same state, -1 if none
-// info: per tile, the kInfo bits.  flags: per tile and slab, how far it is.  ctl: the counter that
-// hands out tiles (64 bits), and a word that stops every wait once one has run out of time.
+// info: per tile, the kInfo bits.  flags: per tile and slab, whether its nodes' rows are written (those
+// that breaks start from; backward, those of its breaks).  ctl: the counter that hands out tiles (64
+// bits), and a word that stops every wait once one has run out of time.
 struct ScanWork {
   int32_t *link, *end, *kid, *sib, *info, *flags, *ctl;
   float *maps, *dnode, *carry;
@@ -74,7 +74,10 @@ enum : int {
   kInfoOut = 32,        // the tile behind follows on its last token
   kInfoSerialBack = 64, // a node's further child, or a break's next sibling, starts in this tile
 };
-enum : int { kFlagMap = 1, kFlagState = 2, kFlagAll = 3 };   // map, state behind it, nodes' rows: published
+// Maps and the states between tiles carry their own arrival: their rows hold this pattern, a NaN that no
+// arithmetic gives, until they are written, and whoever needs one polls the value itself.  No flag and no
+// fence stands between a tile and the next.
+constexpr uint32_t kEmpty = 0xffffffffu;
 
 // the tile is a plain map of the state before it / of the gradient behind it
 DEVI bool is_map_fwd(int info) { return !(info & kInfoBreak); }
@@ -95,15 +98,30 @@ DEVI int link_of(int j, const ScanTree& t) {
   return t.tok_start[a] + t.node_len[a] == j ? kLinkChain : a;
 }
 
-// One block a tile: links and info, the tile's flags cleared; and the rows that no tile writes are
-// zeroed: those of nodes without tokens, and with `inner` of nodes that do not start from nothing.
+// Blocks (tile, share of the channels): links and info, the tile's flags cleared, its map and the state
+// behind it marked empty; and the rows that no tile writes are zeroed: those of nodes without tokens, and
+// with `inner` of nodes that do not start from nothing.
 __global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, int slabs, int C, int inner,
-                                                       float* rows) {
+                                                       float* rows, float* between) {
   __shared__ int bits;
   const int k = blockIdx.x, j = k * TILE + threadIdx.x;
+  {
+    const uint4 e = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
+    const int first = blockIdx.y * TILE + threadIdx.x, step = gridDim.y * TILE;
+    uint4* m = reinterpret_cast<uint4*>(w.maps + (size_t)k * C * 2);
+    uint4* b = reinterpret_cast<uint4*>(between + (size_t)k * C);
+    for (int i = first; i < C / 2; i += step) m[i] = e;
+    for (int i = first; i < C / 4; i += step) b[i] = e;
+    for (int i = first; i < slabs; i += step) w.flags[(size_t)k * slabs + i] = 0;
+  }
+  if (rows)
+    for (int v = k; v < t.n_nodes; v += gridDim.x) {
+      if (t.node_len[v] > 0 && !(inner && scan_token_ancestor(v, t) >= 0)) continue;
+      for (int c = blockIdx.y * TILE + threadIdx.x; c < C; c += gridDim.y * TILE) rows[(size_t)v * C + c] = 0.f;
+    }
+  if (blockIdx.y) return;
   if (threadIdx.x == 0) bits = 0;
   if (k == 0 && threadIdx.x < 4) w.ctl[threadIdx.x] = 0;
-  for (int i = threadIdx.x; i < slabs; i += TILE) w.flags[(size_t)k * slabs + i] = 0;
   __syncthreads();
   if (j < t.N) {
     const int v = t.tok_node[j];
@@ -140,49 +158,118 @@ __global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, i
   }
   __syncthreads();
   if (threadIdx.x == 0) w.info[k] = bits;
-  if (!rows) return;
-  for (int v = k; v < t.n_nodes; v += gridDim.x) {
-    if (t.node_len[v] > 0 && !(inner && scan_token_ancestor(v, t) >= 0)) continue;
-    for (int c = threadIdx.x; c < C; c += TILE) rows[(size_t)v * C + c] = 0.f;
-  }
 }
 
-// p and b of one token
-template <int KIND>
-DEVI void gate_of(float g, float x, float& p, float& b) {
-  if (KIND == TREE_GATE_SIGMOID) {
-    const float e = expf(-fabsf(g)), r = __frcp_rn(1.f + e);
-    const float small = e * r;                       // the smaller of a and 1 - a
-    p = g > 0.f ? -small : small;
-    b = (g > 0.f ? small : r) * x;
-  } else {
-    const float q = g > 0.f ? 0.f : g;               // NaN stays NaN
-    const float m = expm1f(q);
-    p = m > -0.5f ? m : expf(q);
-    if (m == 0.f) p = -0.f;
-    b = x;
-  }
+// A lane's one or two channels of a value; pairs go through the packed fp32 instructions.
+template <int CH>
+struct Vec {
+  float v[CH];
+};
+template <int CH>
+DEVI Vec<CH> vec(float a) {
+  Vec<CH> r;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) r.v[c] = a;
+  return r;
 }
+DEVI Vec<1> operator+(Vec<1> a, Vec<1> b) { return {{a.v[0] + b.v[0]}}; }
+DEVI Vec<1> operator*(Vec<1> a, Vec<1> b) { return {{a.v[0] * b.v[0]}}; }
+DEVI Vec<1> vfma(Vec<1> a, Vec<1> b, Vec<1> c) { return {{fmaf(a.v[0], b.v[0], c.v[0])}}; }
+DEVI uint64_t f2(Vec<2> a) { return f2_pack(a.v[0], a.v[1]); }
+DEVI Vec<2> f2(uint64_t a) {
+  Vec<2> r;
+  f2_unpack(a, r.v[0], r.v[1]);
+  return r;
+}
+DEVI Vec<2> operator+(Vec<2> a, Vec<2> b) { return f2(f2_add(f2(a), f2(b))); }
+DEVI Vec<2> operator*(Vec<2> a, Vec<2> b) { return f2(f2_mul(f2(a), f2(b))); }
+DEVI Vec<2> vfma(Vec<2> a, Vec<2> b, Vec<2> c) { return f2(f2_fma(f2(a), f2(b), f2(c))); }
+template <int CH>
+DEVI Vec<CH> operator-(Vec<CH> a) {
+#pragma unroll
+  for (int c = 0; c < CH; ++c) a.v[c] = -a.v[c];
+  return a;
+}
+template <int CH>
+DEVI Vec<CH> operator-(Vec<CH> a, Vec<CH> b) { return a + (-b); }
+
+// A decay a as p: -(1 - a) with the sign bit set where a >= 1/2, a itself elsewhere.
 DEVI bool near_one(float p) { return __float_as_int(p) < 0; }
-DEVI float decay(float p) { return near_one(p) ? 1.f + p : p; }
-DEVI float lack(float p) { return near_one(p) ? -p : 1.f - p; }
-// a h + b
-DEVI float scan_step(float p, float b, float h) { return fmaf(p, h, b) + (near_one(p) ? h : 0.f); }
+template <int CH>
+DEVI Vec<CH> pick(Vec<CH> p, Vec<CH> a, Vec<CH> b) {      // a where the decay is near one, else b
+#pragma unroll
+  for (int c = 0; c < CH; ++c) a.v[c] = near_one(p.v[c]) ? a.v[c] : b.v[c];
+  return a;
+}
 // a h
-DEVI float scan_mul(float p, float h) { return fmaf(p, h, near_one(p) ? h : 0.f); }
-// b, from x and p
-template <int KIND>
-DEVI float input_of(float p, float x) { return KIND == TREE_GATE_SIGMOID ? lack(p) * x : x; }
+template <int CH>
+DEVI Vec<CH> decayed(Vec<CH> p, Vec<CH> h) { return vfma(p, h, pick(p, h, vec<CH>(0.f))); }
+// a h + b.  Sigmoid gate: a h + (1 - a) x is h + p (h - x) or x + p (h - x).
+template <int KIND, int CH>
+DEVI Vec<CH> advance(Vec<CH> p, Vec<CH> x, Vec<CH> h) {
+  if (KIND == TREE_GATE_SIGMOID) return vfma(p, h - x, pick(p, h, x));
+  return vfma(p, h, pick(p, h, vec<CH>(0.f)) + x);
+}
 
-template <int KIND>
-DEVI void gate_grad(float g, float x, float p, float before, float lam, float& dg, float& dx) {
+DEVI float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEVI float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEVI float rcp_approx(float a) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+// e^n for -100 <= n <= 0: 2^t of the hardware (2 units in the last place) at t = n log2(e) rounded, and the
+// first-order term of what the rounding took from n
+template <int CH>
+DEVI Vec<CH> exp_of(Vec<CH> n) {
+  const Vec<CH> t = n * vec<CH>(1.4426950408889634f), r = vfma(t, vec<CH>(-0.6931471805599453f), n);
+  Vec<CH> e;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) e.v[c] = ex2_approx(t.v[c]);
+  return vfma(e, r, e);
+}
+// p of gate values g
+template <int KIND, int CH>
+DEVI Vec<CH> gate_of(Vec<CH> g) {
+  Vec<CH> n, p;
   if (KIND == TREE_GATE_SIGMOID) {
-    dx = lam * lack(p);
-    dg = dx * decay(p) * (before - x);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) n.v[c] = max_nan(-fabsf(g.v[c]), -100.f);
+    const Vec<CH> e = exp_of(n), d = e + vec<CH>(1.f);
+    Vec<CH> q;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) q.v[c] = rcp_approx(d.v[c]);
+    q = e * q;                                        // the smaller of a and 1 - a; it is 1 - a where g >= 0
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      p.v[c] = __uint_as_float(__float_as_uint(q.v[c]) ^ (~__float_as_uint(g.v[c]) & 0x80000000u));
   } else {
-    dx = lam;
-    dg = g > 0.f ? 0.f : lam * decay(p) * before;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) n.v[c] = max_nan(min_nan(g.v[c], 0.f), -100.f);
+    const Vec<CH> e = exp_of(n);
+    // e^n - 1 for n > -ln 2: the series n + n^2/2! + ... + n^9/9!, whose next term is below 2^-26 of the sum
+    Vec<CH> s = vec<CH>(1.f / 362880);
+    s = vfma(s, n, vec<CH>(1.f / 40320));
+    s = vfma(s, n, vec<CH>(1.f / 5040));
+    s = vfma(s, n, vec<CH>(1.f / 720));
+    s = vfma(s, n, vec<CH>(1.f / 120));
+    s = vfma(s, n, vec<CH>(1.f / 24));
+    s = vfma(s, n, vec<CH>(1.f / 6));
+    s = vfma(s, n, vec<CH>(0.5f));
+    s = vfma(n * n, s, n);
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      p.v[c] = n.v[c] <= -0.6931471805599453f ? e.v[c] : __uint_as_float(__float_as_uint(s.v[c]) | 0x80000000u);
   }
+  return p;
 }
 
 // A lane's word of a row: two bf16 channels or one fp32 channel.
@@ -191,64 +278,117 @@ struct Lane;
 template <>
 struct Lane<__nv_bfloat16> {
   static constexpr int CH = 2;
-  static DEVI void unpack(uint32_t w, float (&v)[2]) { v[0] = bf16lo(w); v[1] = bf16hi(w); }
-  static DEVI uint32_t pack(const float (&v)[2]) { return pack_bf16(v[0], v[1]); }
+  static DEVI Vec<2> unpack(uint32_t w) { return {{bf16lo(w), bf16hi(w)}}; }
+  static DEVI uint32_t pack(Vec<2> a) { return pack_bf16(a.v[0], a.v[1]); }
 };
 template <>
 struct Lane<float> {
   static constexpr int CH = 1;
-  static DEVI void unpack(uint32_t w, float (&v)[1]) { v[0] = __uint_as_float(w); }
-  static DEVI uint32_t pack(const float (&v)[1]) { return __float_as_uint(v[0]); }
+  static DEVI Vec<1> unpack(uint32_t w) { return {{__uint_as_float(w)}}; }
+  static DEVI uint32_t pack(Vec<1> a) { return __float_as_uint(a.v[0]); }
 };
 // fp32 values of a lane's channels, past L1 (another block may have written them)
-DEVI void ld_state(const float* p, float (&v)[2]) { const float2 a = __ldcg(reinterpret_cast<const float2*>(p)); v[0] = a.x; v[1] = a.y; }
-DEVI void ld_state(const float* p, float (&v)[1]) { v[0] = __ldcg(p); }
-// the same where `want`, else zeros; loads of a run of calls are all in flight before the first is used
-DEVI void ld_state_if(const float* p, bool want, float (&v)[2]) {
+// where `want`, else zeros; loads of a run of calls are all in flight before the first is used
+DEVI Vec<2> ld_state_if(const float* p, bool want, Vec<2>) {
+  Vec<2> r;
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
                "@q ld.global.cg.v2.f32 {%0, %1}, [%2];\n\t}"
-               : "=&f"(v[0]), "=&f"(v[1]) : "l"(p), "r"((uint32_t)want) : "memory");
+               : "=&f"(r.v[0]), "=&f"(r.v[1]) : "l"(p), "r"((uint32_t)want) : "memory");
+  return r;
 }
-DEVI void ld_state_if(const float* p, bool want, float (&v)[1]) {
+DEVI Vec<1> ld_state_if(const float* p, bool want, Vec<1>) {
+  Vec<1> r;
   asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\tmov.f32 %0, 0f00000000;\n\t"
                "@q ld.global.cg.f32 %0, [%1];\n\t}"
-               : "=&f"(v[0]) : "l"(p), "r"((uint32_t)want) : "memory");
+               : "=&f"(r.v[0]) : "l"(p), "r"((uint32_t)want) : "memory");
+  return r;
 }
-DEVI void st_state(float* p, const float (&v)[2]) { __stcg(reinterpret_cast<float2*>(p), make_float2(v[0], v[1])); }
-DEVI void st_state(float* p, const float (&v)[1]) { __stcg(p, v[0]); }
-// a lane's maps (A, B per channel)
-DEVI void ld_map(const float* p, float (&A)[2], float (&B)[2]) {
-  const float4 a = __ldcg(reinterpret_cast<const float4*>(p));
-  A[0] = a.x; B[0] = a.y; A[1] = a.z; B[1] = a.w;
+DEVI void st_state(float* p, Vec<2> v) { __stcg(reinterpret_cast<float2*>(p), make_float2(v.v[0], v.v[1])); }
+DEVI void st_state(float* p, Vec<1> v) { __stcg(p, v.v[0]); }
+// Values that other blocks wait for: a lane's state, and its map h -> A h + B as (A, B) per channel.  Each
+// word arrives by itself.
+DEVI float full_word(float v) { return __float_as_uint(v) == kEmpty ? __uint_as_float(0x7fffffffu) : v; }
+DEVI bool is_full(float v) { return __float_as_uint(v) != kEmpty; }
+DEVI bool is_full(Vec<2> v) { return is_full(v.v[0]) && is_full(v.v[1]); }
+DEVI bool is_full(Vec<1> v) { return is_full(v.v[0]); }
+DEVI void hand_state(float* p, Vec<2> v) {
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(full_word(v.v[0])), "f"(full_word(v.v[1])) : "memory");
 }
-DEVI void ld_map(const float* p, float (&A)[1], float (&B)[1]) { const float2 a = __ldcg(reinterpret_cast<const float2*>(p)); A[0] = a.x; B[0] = a.y; }
-DEVI void st_map(float* p, const float (&A)[2], const float (&B)[2]) { __stcg(reinterpret_cast<float4*>(p), make_float4(A[0], B[0], A[1], B[1])); }
-DEVI void st_map(float* p, const float (&A)[1], const float (&B)[1]) { __stcg(reinterpret_cast<float2*>(p), make_float2(A[0], B[0])); }
+DEVI void hand_state(float* p, Vec<1> v) {
+  asm volatile("st.relaxed.gpu.global.f32 [%0], %1;" ::"l"(p), "f"(full_word(v.v[0])) : "memory");
+}
+DEVI Vec<2> look_state(const float* p, Vec<2>) {
+  Vec<2> r;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(r.v[0]), "=f"(r.v[1]) : "l"(p) : "memory");
+  return r;
+}
+DEVI Vec<1> look_state(const float* p, Vec<1>) {
+  Vec<1> r;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(r.v[0]) : "l"(p) : "memory");
+  return r;
+}
+DEVI void hand_map(float* p, Vec<2> A, Vec<2> B) {
+  asm volatile("st.relaxed.gpu.global.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(full_word(A.v[0])),
+               "f"(full_word(B.v[0])), "f"(full_word(A.v[1])), "f"(full_word(B.v[1])) : "memory");
+}
+DEVI void hand_map(float* p, Vec<1> A, Vec<1> B) {
+  asm volatile("st.relaxed.gpu.global.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(full_word(A.v[0])), "f"(full_word(B.v[0])) : "memory");
+}
+DEVI void look_map(const float* p, Vec<2>& A, Vec<2>& B) {
+  asm volatile("ld.relaxed.gpu.global.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(A.v[0]), "=f"(B.v[0]), "=f"(A.v[1]), "=f"(B.v[1]) : "l"(p) : "memory");
+}
+DEVI void look_map(const float* p, Vec<1>& A, Vec<1>& B) {
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(A.v[0]), "=f"(B.v[0]) : "l"(p) : "memory");
+}
+template <int CH>
+DEVI Vec<CH> sh_ld(const float* p) {
+  Vec<CH> r;
+  const int lane = threadIdx.x & 31;
+  if constexpr (CH == 2) {
+    const float2 a = reinterpret_cast<const float2*>(p)[lane];
+    r.v[0] = a.x;
+    r.v[1] = a.y;
+  } else {
+    r.v[0] = p[lane];
+  }
+  return r;
+}
+template <int CH>
+DEVI void sh_st(float* p, Vec<CH> a) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (CH == 2) reinterpret_cast<float2*>(p)[lane] = make_float2(a.v[0], a.v[1]);
+  else p[lane] = a.v[0];
+}
 
 DEVI int ld_acquire(const int32_t* p) {
   int v;
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-DEVI void st_release(int32_t* p, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+DEVI void set_release(int32_t* p, int bits) {      // *p |= bits, after everything before it
+  asm volatile("red.release.gpu.global.or.b32 [%0], %1;" ::"l"(p), "r"(bits) : "memory");
 }
 
-// Wait until *flag is at least `want`.  The first wait of the grid that runs out of time stops all others.
-DEVI bool wait_flag(const int32_t* flag, int want, const WaitCtl& wc, int32_t* stop) {
-  if (ld_acquire(flag) >= want) return true;
+// Wait until look() is true.  The first wait of the grid that runs out of time stops all others.
+template <typename Look>
+DEVI bool wait_until(Look look, const WaitCtl& wc, int32_t* stop) {
+  if (look()) return true;
   const uint64_t t0 = global_timer_ns();
   for (uint32_t it = 1;; ++it) {
-    if (ld_acquire(flag) >= want) return true;
+    if (look()) return true;
     if ((it & 15u) == 0) {
       if (*wc.abort_flag || ld_acquire(stop)) return false;
       if (global_timer_ns() - t0 > wc.limit_ns) {
         if (wc.status) atomicExch(wc.status, TREE_ERR_TIMEOUT);
-        st_release(stop, 1);
+        set_release(stop, 1);
         return false;
       }
     }
   }
+}
+// ... until a tile's node rows are written
+DEVI bool wait_rows(const int32_t* flag, const WaitCtl& wc, int32_t* stop) {
+  return wait_until([&] { return ld_acquire(flag) != 0; }, wc, stop);
 }
 
 DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
@@ -283,16 +423,19 @@ struct ScanBwd {
   uint64_t limit_ns;
 };
 
-// Shared by both kernels: a ring of stages, each one tile's rows of ARRAYS tensors.
+// Shared by both kernels: a ring of stages, each one tile's rows of the staged tensors, and what the warps
+// of a block tell each other, twice over: a warp may be a tile ahead of another.
 template <int STAGES>
 struct ScanShared {
-  uint64_t full[STAGES], empty[STAGES];
+  uint64_t full[STAGES], empty[STAGES], ready[2];  // ready: the state before (gradient behind) the tile is in `in`
   int tile[STAGES], slab[STAGES], info[STAGES], dist[STAGES];
   int abort_flag;
-  int reset[kScanWarps];
-  alignas(16) float maps[kScanWarps][64][2];       // per warp and channel: A, B
-  float back[kScanWarps][64];                      // backward: what the warp adds to the gradient
-  float in[64];
+  int in_ok[2], reset[2][kScanWarps];
+  alignas(16) float A[2][kScanWarps][64];          // per warp and channel: the map of its 16 tokens
+  alignas(16) float B[2][kScanWarps][64];
+  alignas(16) float R[2][kScanWarps][64];          // backward: that of the gradient is u -> A u + R
+  alignas(16) float in[2][64];
+  alignas(16) float carry[kScanWarps][64];         // behind (before) a warp, in tiles that go warp by warp
 };
 
 // The loading warp: takes tiles from the counter, starts their copies, and finds how many maps lie
@@ -308,6 +451,9 @@ DEVI void scan_loader(ScanShared<STAGES>& sh, uint8_t* stages, const CUtensorMap
   for (; live; ++i) {
     const int s = i % STAGES;
     bool ok = true;
+    // The second ticket waits for the first one's copies: all blocks have their first by then.  A block that
+    // took two neighbouring tiles at once would keep the second's map back while others wait for it.
+    if (lane == 0 && i == 1) ok = mbar_wait(&sh.full[0], 0, wc);
     if (lane == 0 && i >= STAGES) ok = mbar_wait(&sh.empty[s], ((i / STAGES) - 1) & 1, wc);
     if (!__all_sync(0xffffffffu, ok)) break;
     unsigned long long ticket = 0;
@@ -353,465 +499,472 @@ DEVI void scan_loader(ScanShared<STAGES>& sh, uint8_t* stages, const CUtensorMap
     }
 }
 
-// Join `dist` maps to the state (or gradient) behind tile b, in the order in which the recurrence
-// passes them; tiles b, b + step, ...  One warp; v holds the result.  False if a wait gave up.
+
+constexpr int kBarMaps = 1;                // compute and joining warps: the tile's maps are in shared memory
+constexpr int kBarTurn = 2;                // ... + warp: the warp before (behind) is done, in tiles that go warp by warp
+constexpr int kBarDone = kBarTurn + kScanWarps;     // compute warps: the tile's rows are written
+constexpr int kComputeThreads = 32 * kScanWarps, kMapThreads = kComputeThreads + 32;
+
+DEVI void bar_sync(int id, int threads) {
+  __syncwarp();
+  named_bar_sync(id, threads);
+}
+DEVI void bar_arrive(int id, int threads) {
+  __syncwarp();
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+DEVI bool bar_agree(int id, int threads, bool ok) {        // true where every thread's is
+  __syncwarp();
+  return named_bar_and(id, threads, ok);
+}
+
+// The warp's writes so far, and those that a barrier ordered before them, become visible with the flag.
+DEVI void publish(int32_t* flag) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) set_release(flag, 1);
+}
+
+// The joining warp's part of a tile: the state before it (backward: the gradient behind it), from the state
+// behind tile b and the maps of the `dist` tiles between, in the order in which the recurrence passes them;
+// b, b + step, ... lead to the tile.  The maps are joined first, so that a state that arrives last is one
+// step away from being handed on.
 template <int CH>
-DEVI bool join_maps(float (&v)[CH], int b, int step, int dist, const float* state, const ScanWork& w, int slabs, int slab,
-                    int C, int ch, bool on, const WaitCtl& wc) {
-  const int lane = threadIdx.x & 31;
-  bool ok = true;
-  if (lane <= dist)
-    ok = wait_flag(w.flags + (size_t)(b + step * lane) * slabs + slab, lane == 0 ? kFlagState : kFlagMap, wc,
-                   w.ctl + 2);
-  if (!__all_sync(0xffffffffu, ok)) return false;
-  if (on) {
-    ld_state(state, v);
-#pragma unroll 4
-    for (int j = 1; j <= dist; ++j) {
-      float A[CH], B[CH];
-      ld_map(w.maps + ((size_t)(b + step * j) * C + ch) * 2, A, B);
+struct Joiner {
+  const ScanWork& w;
+  int C, ch, b, step, dist;
+  const float* state;                        // row of tile b, at the lane's channels
+  bool on;
+  static constexpr int BATCH = 5;
+  DEVI const float* map(int j) const { return w.maps + ((size_t)(b + step * j) * C + ch) * 2; }
+  // The joined state in v.  block: wait for what is missing; else false if anything is.
+  DEVI bool join(Vec<CH>& v, bool block, const WaitCtl& wc) const {
+    bool ok = true;
+    Vec<CH> PA = vec<CH>(1.f), PB = vec<CH>(0.f);
+    if (on) {
+      for (int j0 = 1; j0 <= dist && ok; j0 += BATCH) {
+        Vec<CH> A[BATCH], B[BATCH];
 #pragma unroll
-      for (int c = 0; c < CH; ++c) v[c] = fmaf(A[c], v[c], B[c]);
+        for (int q = 0; q < BATCH; ++q)
+          if (j0 + q <= dist) look_map(map(j0 + q), A[q], B[q]);
+#pragma unroll
+        for (int q = 0; q < BATCH; ++q) {
+          if (j0 + q > dist) break;
+          if (!(is_full(A[q]) && is_full(B[q])))
+            ok = block && ok && wait_until([&] { look_map(map(j0 + q), A[q], B[q]); return is_full(A[q]) && is_full(B[q]); },
+                                           wc, w.ctl + 2);
+          PB = vfma(A[q], PB, B[q]);
+          PA = PA * A[q];
+        }
+      }
+      if (ok) {
+        Vec<CH> u = look_state(state, v);
+        if (!is_full(u))
+          ok = block && wait_until([&] { u = look_state(state, u); return is_full(u); }, wc, w.ctl + 2);
+        v = dist ? vfma(PA, u, PB) : u;
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  }
+};
+
+// The joining warp's loop body, both directions: find the state before the tile (ahead of the compute
+// warps where the tiles it needs are done), publish the tile's map and the state behind it.
+// Returns false when the block has to stop.
+template <bool FWD, int CH, int STAGES>
+DEVI bool scan_join(ScanShared<STAGES>& sh, int i, const ScanWork& w, int C, int tiles, int slabs, float* rows, int slab_ch,
+                    const WaitCtl& wc, bool& ok) {
+  const int lane = threadIdx.x & 31, s = i % STAGES, buf = i & 1;
+  ok = mbar_wait_warp(&sh.full[s], (i / STAGES) & 1, wc) && ok;
+  int k = -1, slab = 0, info = 0, dist = 0;
+  if (ok) { k = sh.tile[s]; slab = sh.slab[s]; info = sh.info[s]; dist = sh.dist[s]; }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.empty[s]);
+  const bool live = ok && k >= 0;
+  const int ch = slab * slab_ch + lane * CH;
+  const bool on = live && ch < C;
+  const bool need = live && (info & (FWD ? kInfoIn : kInfoOut));
+  const int b = FWD ? k - 1 - dist : k + 1 + dist;
+  const Joiner<CH> j{w, C, ch, b, FWD ? 1 : -1, dist, rows + (size_t)(need ? b : 0) * C + ch, on};
+  Vec<CH> v = vec<CH>(0.f);
+  auto hand_in = [&](bool good) {
+    sh_st<CH>(sh.in[buf], v);
+    if (lane == 0) sh.in_ok[buf] = good;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.ready[buf]);
+  };
+  const bool joined = live && (!need || j.join(v, false, wc));
+  if (joined) hand_in(true);
+  if (!bar_agree(kBarMaps, kMapThreads, ok) || !live) return false;
+  const bool serial = info & (FWD ? kInfoSerial : kInfoSerialBack);
+  Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
+  bool fixed = false;
+  if (!serial) {
+#pragma unroll
+    for (int n = 0; n < kScanWarps; ++n) {
+      const int q = FWD ? n : kScanWarps - 1 - n;
+      const bool r = sh.reset[buf][q];
+      const Vec<CH> qa = sh_ld<CH>(sh.A[buf][q]), qb = sh_ld<CH>(FWD ? sh.B[buf][q] : sh.R[buf][q]);
+      B = r ? qb : vfma(qa, B, qb);
+      A = A * qa;
+      fixed |= r;
     }
   }
-  return true;
-}
-
-// the warp's writes so far, and those that a barrier ordered before them, become visible with the flag
-DEVI void publish(int32_t* flag, int value) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    __threadfence();
-    st_release(flag, value);
+  const bool map = FWD ? is_map_fwd(info) && (k + 1) % kScanGroup != 0 && k + 1 < tiles
+                       : is_map_bwd(info) && k % kScanGroup != 0;
+  if (map && on) hand_map(w.maps + ((size_t)k * C + ch) * 2, A, B);
+  if (!joined) {
+    ok = j.join(v, true, wc);
+    hand_in(ok);
   }
+  if (!serial && ok && on) hand_state(rows + (size_t)k * C + ch, fixed ? B : vfma(A, v, B));
+  return true;                                 // a failed wait ends the block at the next agreement
 }
 
-constexpr int kScanBar = 1;                // the named barrier of the compute warps
-DEVI void scan_sync() {
-  __syncwarp();
-  named_bar_sync(kScanBar, 32 * kScanWarps);
-}
-DEVI bool scan_agree(bool ok) {            // true where every thread's is
-  __syncwarp();
-  return named_bar_and(kScanBar, 32 * kScanWarps, ok);
-}
+// Forward, one tile, a warp 16 consecutive tokens of it.  First half: the maps to each token from the state
+// before the warp, or from its last break.  PLAIN: no break, no node's end, all 128 tokens there.
+template <int CH>
+struct FwdTile {
+  Vec<CH> A[kWarpTokens], B[kWarpTokens];
+  int from, end;
+  uint32_t breaks, ends, reset;              // a bit a token: breaks; ends; breaks that start outside the tile
+};
 
-// One tile of the forward, a warp 16 consecutive tokens of it.  PLAIN: no break, no node's end, all 128
-// tokens there.  False if a wait gave up.
-template <typename T, int KIND, bool PLAIN, int STAGES>
-DEVI bool scan_tile_fwd(const ScanFwd<T>& a, ScanShared<STAGES>& sh, const uint8_t* stage, uint64_t* empty, int k,
-                        int slab, int info, int dist, const WaitCtl& wc) {
-  constexpr int CH = Lane<T>::CH;
+template <typename T, int KIND, bool PLAIN, int STAGES, int CH>
+DEVI bool fwd_first(FwdTile<CH>& f, const ScanFwd<T>& a, ScanShared<STAGES>& sh, const uint8_t* stage,
+                    uint64_t* empty, int buf, int k, int slab, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = slab * (kRowBytes / (int)sizeof(T)) + lane * CH;      // the lane's first channel
   const bool on = ch < a.C;
   const int t0 = k * TILE + warp * kWarpTokens;
-  const bool in = info & kInfoIn, serial = !PLAIN && (info & kInfoSerial);
-  float p[kWarpTokens][CH], b[kWarpTokens][CH];
-  {
-    const uint8_t* gs = stage + (size_t)(warp * kWarpTokens) * a.row_bytes + lane * 4;
-    const uint8_t* xs = gs + kBoxBytes;
-#pragma unroll
-    for (int i = 0; i < kWarpTokens; ++i) {
-      float g[CH], x[CH];
-      Lane<T>::unpack(on ? *reinterpret_cast<const uint32_t*>(gs + i * a.row_bytes) : 0u, g);
-      Lane<T>::unpack(on ? *reinterpret_cast<const uint32_t*>(xs + i * a.row_bytes) : 0u, x);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) gate_of<KIND>(g[c], x[c], p[i][c], b[i][c]);
+  const uint8_t* gs = stage + (size_t)(warp * kWarpTokens) * a.row_bytes + (on ? lane * 4 : 0);
+  const uint8_t* xs = gs + kBoxBytes;
+  bool ok = true;
+  if (!PLAIN) {
+    f.from = kLinkChain;
+    f.end = -1;
+    bool tile = false;
+    if (lane < kWarpTokens && t0 + lane < a.t.N) {
+      f.from = a.w.link[t0 + lane];
+      f.end = a.w.end[t0 + lane];
+      if (f.from >= 0) {
+        const int ts = (a.t.tok_start[f.from] + a.t.node_len[f.from] - 1) / TILE;
+        tile = ts == k;
+        if (!tile) ok = wait_rows(a.w.flags + (size_t)ts * a.slabs + slab, wc, a.w.ctl + 2);
+      }
     }
+    ok = __all_sync(0xffffffffu, ok);
+    f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
+    f.ends = __ballot_sync(0xffffffffu, f.end >= 0);
+    f.reset = f.breaks & ~__ballot_sync(0xffffffffu, tile);
+    if (f.reset) {
+#pragma unroll
+      for (int i = 0; i < kWarpTokens; ++i) {        // what they start from: all loads first
+        const int n = __shfl_sync(0xffffffffu, f.from, i);
+        const float* row = n >= 0 ? a.states + (size_t)n * a.C
+                                  : (a.init && n == kLinkRoot ? a.init + (size_t)a.t.tok_node[t0 + i] * a.C : nullptr);
+        f.B[i] = ld_state_if(row + ch, on && row && ((f.reset >> i) & 1u), f.B[i]);
+      }
+    }
+  }
+  Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
+#pragma unroll
+  for (int i = 0; i < kWarpTokens; ++i) {
+    Vec<CH> p = gate_of<KIND>(Lane<T>::unpack(*reinterpret_cast<const uint32_t*>(gs + i * a.row_bytes)));
+    Vec<CH> x = Lane<T>::unpack(*reinterpret_cast<const uint32_t*>(xs + i * a.row_bytes));
+    if (!PLAIN) {
+      if (t0 > a.t.N - 1 - i) {                      // behind the last token h stays
+        p = vec<CH>(-0.f);
+        x = vec<CH>(0.f);
+      }
+      if ((f.breaks >> i) & 1u) {
+        A = vec<CH>(1.f);
+        B = ((f.reset >> i) & 1u) ? f.B[i] : vec<CH>(0.f);
+      }
+    }
+    B = advance<KIND>(p, x, B);
+    A = decayed(p, A);
+    f.A[i] = A;
+    f.B[i] = B;
   }
   __syncwarp();
   if (lane == 0) mbar_arrive(empty);                 // the stage is in registers
-  // Breaks: `from` per lane and token, the node or kind of start; a start from outside the tile is folded
-  // into its token, whose own map is then the constant b.
-  int from = kLinkChain, end = -1;
-  uint32_t breaks = 0, ends = 0, reset = 0;
-  if (!PLAIN) {
-    const int t = t0 + lane;
-    bool ok = true;
-    if (lane < kWarpTokens && t < a.t.N) {
-      from = a.w.link[t];
-      end = a.w.end[t];
-      if (from >= 0) {
-        const int ts = (a.t.tok_start[from] + a.t.node_len[from] - 1) / TILE;
-        if (ts != k) ok = wait_flag(a.w.flags + (size_t)ts * a.slabs + slab, kFlagAll, wc, a.w.ctl + 2);
-        else from |= kFromTile;                      // a node of this tile: its state comes while the tile runs
-      }
-    }
-    if (!scan_agree(ok)) return false;
-    breaks = __ballot_sync(0xffffffffu, from != kLinkChain);
-    ends = __ballot_sync(0xffffffffu, end >= 0);
-    reset = breaks & ~__ballot_sync(0xffffffffu, from >= 0 && (from & kFromTile));
-    if (t0 > a.t.N - kWarpTokens) {                  // behind the last token h stays
-#pragma unroll
-      for (int i = 0; i < kWarpTokens; ++i)
-        if (t0 + i >= a.t.N) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) { p[i][c] = -0.f; b[i][c] = 0.f; }
-        }
-    }
-    if (reset) {
-      float s[kWarpTokens][CH];
-#pragma unroll
-      for (int i = 0; i < kWarpTokens; ++i) {        // all loads first: none waits for another
-        const int f = __shfl_sync(0xffffffffu, from, i);
-        const float* row = f >= 0 ? a.states + (size_t)(f & ~kFromTile) * a.C
-                                  : (a.init && f == kLinkRoot ? a.init + (size_t)a.t.tok_node[t0 + i] * a.C : nullptr);
-        ld_state_if(row + ch, on && row && ((reset >> i) & 1u), s[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kWarpTokens; ++i)
-        if ((reset >> i) & 1u) {
-#pragma unroll
-          for (int c = 0; c < CH; ++c) b[i][c] = scan_step(p[i][c], b[i][c], s[i][c]);
-        }
-    }
-  }
-  // The warp's 16 steps as one map; behind a reset it is a constant.
-  float A[CH], B[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; }
-  if (!serial) {
-#pragma unroll
-    for (int i = 0; i < kWarpTokens; ++i) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        B[c] = (!PLAIN && ((reset >> i) & 1u)) ? b[i][c] : scan_step(p[i][c], b[i][c], B[c]);
-        A[c] = scan_mul(p[i][c], A[c]);
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      sh.maps[warp][lane * CH + c][0] = A[c];
-      sh.maps[warp][lane * CH + c][1] = B[c];
-    }
-    if (!PLAIN && lane == 0) sh.reset[warp] = reset != 0;
-  }
-  scan_sync();
-  int32_t* flag = a.w.flags + (size_t)k * a.slabs + slab;
-  float* after = a.states + (size_t)(a.t.n_nodes + k) * a.C + ch;       // the state behind the tile
-  const int last_flag = (info & kInfoSource) ? kFlagState : kFlagAll;
-  // The map of the warps before this one (warp 0: of all, for the tile).
-  const int upto = warp == 0 ? kScanWarps : warp;
-  bool fixed = false;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; }
-  if (!serial)
-    for (int q = 0; q < upto; ++q) {
-      const bool r = !PLAIN && sh.reset[q];
-      fixed |= r;
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const float qa = sh.maps[q][lane * CH + c][0], qb = sh.maps[q][lane * CH + c][1];
-        B[c] = r ? qb : fmaf(qa, B[c], qb);
-        A[c] *= qa;
-      }
-    }
-  bool ok = true;
-  if (warp == 0) {
-    if (is_map_fwd(info) && (k + 1) % kScanGroup != 0 && k + 1 < a.tiles) {
-      if (on) st_map(a.w.maps + ((size_t)k * a.C + ch) * 2, A, B);
-      publish(flag, kFlagMap);
-    }
-    float h[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) h[c] = 0.f;
-    if (in) {
-      const int base = k - 1 - dist;
-      ok = join_maps(h, base, 1, dist, a.states + (size_t)(a.t.n_nodes + base) * a.C + ch, a.w, a.slabs, slab, a.C, ch,
-                     on, wc);
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) sh.in[lane * CH + c] = h[c];
-    if (!serial && ok) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) h[c] = fixed ? B[c] : fmaf(A[c], h[c], B[c]);
-      if (on) st_state(after, h);
-      publish(flag, last_flag);
-    }
-    fixed = false;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; }
-  }
-  if (!scan_agree(ok)) return false;
-  // Now every h.
-  float h[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    h[c] = sh.in[lane * CH + c];
-    h[c] = fixed ? B[c] : (warp == 0 ? h[c] : fmaf(A[c], h[c], B[c]));
-  }
-  for (int turn = 0; turn < (serial ? kScanWarps : 1); ++turn) {
-    if (!serial || turn == warp) {
-      if (serial && warp > 0) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) h[c] = sh.in[lane * CH + c];
-      }
-      T* y = a.y + (size_t)t0 * a.C + ch;
-#pragma unroll
-      for (int i = 0; i < kWarpTokens; ++i) {
-        if (!PLAIN && ((breaks >> i) & 1u) && !((reset >> i) & 1u)) {
-          const int f = __shfl_sync(0xffffffffu, from, i) & ~kFromTile;
-          if (on) ld_state(a.states + (size_t)f * a.C + ch, h);
-        }
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          h[c] = (!PLAIN && ((reset >> i) & 1u)) ? b[i][c] : scan_step(p[i][c], b[i][c], h[c]);
-        if (on && (PLAIN || t0 + i < a.t.N)) *reinterpret_cast<uint32_t*>(y + (size_t)i * a.C) = Lane<T>::pack(h);
-        if (!PLAIN && ((ends >> i) & 1u)) {
-          const int e = __shfl_sync(0xffffffffu, end, i);
-          if (on) st_state(a.states + (size_t)e * a.C + ch, h);
-        }
-      }
-      if (serial) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < CH; ++c) sh.in[lane * CH + c] = h[c];
-        if (warp == kScanWarps - 1 && on) st_state(after, h);
-      }
-    }
-    if (serial) scan_sync();
-  }
-  if (!PLAIN && (serial || (info & kInfoSource))) {
-    if (!serial) scan_sync();
-    if (warp == 0) publish(flag, kFlagAll);
-  }
-  return true;
+  sh_st(sh.A[buf][warp], A);
+  sh_st(sh.B[buf][warp], B);
+  if (lane == 0) sh.reset[buf][warp] = !PLAIN && f.reset != 0;
+  return ok;
 }
 
-// One tile of the backward.  h is computed again from the state behind the tile before; the gradient runs
-// from the last token to the first.  PLAIN: no break, nothing joins at a node's end, all 128 tokens there.
-template <typename T, int KIND, bool PLAIN, int STAGES>
-DEVI bool scan_tile_bwd(const ScanBwd<T>& a, ScanShared<STAGES>& sh, const uint8_t* stage, int k, int slab, int info,
-                        int dist, const WaitCtl& wc) {
-  constexpr int CH = Lane<T>::CH;
+// Second half: the state before the warp, then every h.  Where breaks start from nodes that end in this
+// very tile, the warps go one after the other.
+template <typename T, bool PLAIN, int STAGES, int CH>
+DEVI bool fwd_second(const FwdTile<CH>& f, const ScanFwd<T>& a, ScanShared<STAGES>& sh, int buf, uint32_t parity,
+                     int k, int slab, int info, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ch = slab * (kRowBytes / (int)sizeof(T)) + lane * CH;
-  const bool on = ch < a.C;
+  const bool on = ch < a.C, serial = !PLAIN && (info & kInfoSerial);
   const int t0 = k * TILE + warp * kWarpTokens;
-  const bool serial = !PLAIN && (info & kInfoSerialBack);
-  const uint8_t* gs = stage + (size_t)(warp * kWarpTokens) * a.row_bytes + lane * 4;
-  const uint8_t *xs = gs + kBoxBytes, *ds = xs + kBoxBytes;
-  auto word = [&](const uint8_t* q, int i, float(&v)[CH]) {
-    Lane<T>::unpack(on ? *reinterpret_cast<const uint32_t*>(q + i * a.row_bytes) : 0u, v);
-  };
-  float hin[CH];                                     // the state before the tile
-  ld_state_if(a.states + (size_t)(a.t.n_nodes + k - 1) * a.C + ch, on && (info & kInfoIn), hin);
-  float p[kWarpTokens][CH], before[kWarpTokens][CH];
-  int from = kLinkChain, end = -1, kid = -1, sib = -1, own = -1;
-  uint32_t breaks = 0, ends = 0;
-  if (!PLAIN) {
-    const int t = t0 + lane;
-    bool ok = true;
-    if (lane < kWarpTokens && t < a.t.N) {
-      from = a.w.link[t];
-      end = a.w.end[t];
-      kid = a.w.kid[t];
-      sib = a.w.sib[t];
-      own = a.t.tok_node[t];
-      if (kid >= 0) {
-        const int tk = a.t.tok_start[kid] / TILE;
-        if (tk != k) ok = wait_flag(a.w.flags + (size_t)tk * a.slabs + slab, kFlagAll, wc, a.w.ctl + 2);
+  Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
+  bool fixed = false;
+  if (!serial) {
+#pragma unroll
+    for (int q = 0; q < kScanWarps - 1; ++q) {
+      if (q >= warp) break;
+      const bool r = !PLAIN && sh.reset[buf][q];
+      const Vec<CH> qa = sh_ld<CH>(sh.A[buf][q]), qb = sh_ld<CH>(sh.B[buf][q]);
+      B = r ? qb : vfma(qa, B, qb);
+      A = A * qa;
+      fixed |= r;
+    }
+  }
+  bool ok = mbar_wait_warp(&sh.ready[buf], parity, wc) && sh.in_ok[buf];
+  Vec<CH> h = sh_ld<CH>(sh.in[buf]);                 // the state before the tile
+  if (!serial) {
+    if (warp > 0) h = fixed ? B : vfma(A, h, B);
+  } else if (warp > 0) {
+    bar_sync(kBarTurn + warp, 64);
+    h = sh_ld<CH>(sh.carry[warp - 1]);
+  }
+  T* y = a.y + (size_t)t0 * a.C + ch;
+  if (PLAIN) {
+    if (on && ok) {
+#pragma unroll
+      for (int i = 0; i < kWarpTokens; ++i)
+        *reinterpret_cast<uint32_t*>(y + (size_t)i * a.C) = Lane<T>::pack(vfma(f.A[i], h, f.B[i]));
+    }
+    return ok;
+  }
+  // Walk over the tokens: h the state that the run at hand started from, `set` where that is in B already.
+  auto walk = [&](Vec<CH> h, bool write_y, bool write_ends) {
+    bool set = false;
+    Vec<CH> v = h;
+#pragma unroll
+    for (int i = 0; i < kWarpTokens; ++i) {
+      if ((f.breaks >> i) & 1u) {
+        set = (f.reset >> i) & 1u;
+        if (!set) h = ld_state_if(a.states + (size_t)__shfl_sync(0xffffffffu, f.from, i) * a.C + ch, on, h);
       }
-      if (ok && sib >= 0) {
-        const int tk = a.t.tok_start[sib] / TILE;
-        if (tk != k) ok = wait_flag(a.w.flags + (size_t)tk * a.slabs + slab, kFlagAll, wc, a.w.ctl + 2);
+      v = set ? f.B[i] : vfma(f.A[i], h, f.B[i]);
+      if (write_y && on && t0 + i < a.t.N) *reinterpret_cast<uint32_t*>(y + (size_t)i * a.C) = Lane<T>::pack(v);
+      if (write_ends && ((f.ends >> i) & 1u)) {
+        const int e = __shfl_sync(0xffffffffu, f.end, i);
+        if (on) st_state(a.states + (size_t)e * a.C + ch, v);
       }
     }
-    if (!scan_agree(ok)) return false;
-    breaks = __ballot_sync(0xffffffffu, from != kLinkChain);
-    ends = __ballot_sync(0xffffffffu, kid >= 0 || (end >= 0 && a.d_final));
-    if (breaks) {
+    return v;
+  };
+  int32_t* flag = a.w.flags + (size_t)k * a.slabs + slab;
+  if (!serial) {
+    if (ok) walk(h, true, true);
+    if (info & kInfoSource) {
+      bar_sync(kBarDone, kComputeThreads);
+      if (warp == 0 && ok) publish(flag);
+    }
+    return ok;
+  }
+  // what the next warps wait for first: ends and the state behind the warp
+  const Vec<CH> v = ok ? walk(h, false, true) : h;
+  if (warp < kScanWarps - 1) {
+    sh_st(sh.carry[warp], v);
+    bar_arrive(kBarTurn + warp + 1, 64);
+  } else if (ok) {
+    if (on) hand_state(a.states + (size_t)(a.t.n_nodes + k) * a.C + ch, v);
+    publish(flag);
+  }
+  if (ok) walk(h, true, false);
+  return ok;
+}
+
+// Backward, one tile.  First half: p of every token, and the warp's 16 steps as a map of h and as one of the
+// gradient.  PLAIN: no break, nothing joins at a node's end, all 128 tokens there.
+template <int CH>
+struct BwdTile {
+  Vec<CH> p[kWarpTokens], before[kWarpTokens];
+  Vec<CH> hin;
+  int from, end, kid, sib, own;
+  uint32_t breaks, ends;
+};
+
+// A warp's rows of a stage: word i of the gate's, x's and dy's
+template <typename T>
+struct Rows {
+  const uint8_t* base;
+  int stride;
+  template <int WHICH>
+  DEVI Vec<Lane<T>::CH> at(int i) const {
+    return Lane<T>::unpack(*reinterpret_cast<const uint32_t*>(base + WHICH * kBoxBytes + i * stride));
+  }
+};
+
+// what joins the gradient at token i besides dy and the token behind it
+template <typename T, int CH>
+DEVI Vec<CH> joins_at(const BwdTile<CH>& f, const ScanBwd<T>& a, int i, int ch, bool on) {
+  const int kd = __shfl_sync(0xffffffffu, f.kid, i), e = __shfl_sync(0xffffffffu, f.end, i);
+  const Vec<CH> d = ld_state_if(a.d_final + (size_t)e * a.C + ch, on && a.d_final, Vec<CH>());
+  return d + ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on && kd >= 0, Vec<CH>());
+}
+
+template <typename T, int KIND, bool PLAIN, int STAGES, int CH>
+DEVI bool bwd_first(BwdTile<CH>& f, const ScanBwd<T>& a, ScanShared<STAGES>& sh, const Rows<T>& rows, int buf, int k,
+                    int slab, int info, const WaitCtl& wc) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ch = slab * (kRowBytes / (int)sizeof(T)) + lane * CH;
+  const bool on = ch < a.C, serial = !PLAIN && (info & kInfoSerialBack);
+  const int t0 = k * TILE + warp * kWarpTokens;
+  bool ok = true;
+  f.hin = ld_state_if(a.states + (size_t)(a.t.n_nodes + k - 1) * a.C + ch, on && (info & kInfoIn), f.hin);
+  f.breaks = f.ends = 0;
+  if (!PLAIN) {
+    f.from = kLinkChain;
+    f.end = f.kid = f.sib = f.own = -1;
+    if (lane < kWarpTokens && t0 + lane < a.t.N) {
+      const int t = t0 + lane;
+      f.from = a.w.link[t];
+      f.end = a.w.end[t];
+      f.kid = a.w.kid[t];
+      f.sib = a.w.sib[t];
+      f.own = a.t.tok_node[t];
+      if (f.kid >= 0) {
+        const int tk = a.t.tok_start[f.kid] / TILE;
+        if (tk != k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + slab, wc, a.w.ctl + 2);
+      }
+      if (ok && f.sib >= 0) {
+        const int tk = a.t.tok_start[f.sib] / TILE;
+        if (tk != k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + slab, wc, a.w.ctl + 2);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok);
+    f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
+    f.ends = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
+    if (f.breaks) {
 #pragma unroll
       for (int i = 0; i < kWarpTokens; ++i) {        // where a break's h comes from
-        const int f = __shfl_sync(0xffffffffu, from, i), v = __shfl_sync(0xffffffffu, own, i);
-        const float* row = f >= 0 ? a.states + (size_t)f * a.C
-                                  : (a.init && f == kLinkRoot ? a.init + (size_t)v * a.C : nullptr);
-        ld_state_if(row + ch, on && row && ((breaks >> i) & 1u), before[i]);
+        const int n = __shfl_sync(0xffffffffu, f.from, i), v = __shfl_sync(0xffffffffu, f.own, i);
+        const float* row = n >= 0 ? a.states + (size_t)n * a.C
+                                  : (a.init && n == kLinkRoot ? a.init + (size_t)v * a.C : nullptr);
+        f.before[i] = ld_state_if(row + ch, on && row && ((f.breaks >> i) & 1u), f.before[i]);
       }
     }
   }
-  // what joins the gradient at token i besides dy and the token behind it
-  auto joins = [&](int i, float(&v)[CH]) {
-    const int kd = __shfl_sync(0xffffffffu, kid, i), e = __shfl_sync(0xffffffffu, end, i);
-    float r[CH];
-    if (a.d_final) {
-      ld_state_if(a.d_final + (size_t)e * a.C + ch, on, r);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) v[c] += r[c];
-    }
-    ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on && kd >= 0, r);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) v[c] += r[c];
-  };
-  // The warp's 16 steps as one map of h, and as one of the gradient (with the same factor).
-  float A[CH], B[CH], R[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) { A[c] = 1.f; B[c] = 0.f; R[c] = 0.f; }
+  Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f), R = vec<CH>(0.f);
 #pragma unroll
   for (int i = 0; i < kWarpTokens; ++i) {
-    float g[CH], x[CH];
-    word(gs, i, g);
-    word(xs, i, x);
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float b;
-      gate_of<KIND>(g[c], x[c], p[i][c], b);
-      B[c] = scan_step(p[i][c], b, (!PLAIN && ((breaks >> i) & 1u)) ? before[i][c] : B[c]);
-      A[c] = scan_mul(p[i][c], A[c]);
-    }
+    f.p[i] = gate_of<KIND>(rows.template at<0>(i));
+    if (!PLAIN && ((f.breaks >> i) & 1u)) B = f.before[i];
+    B = advance<KIND>(f.p[i], rows.template at<1>(i), B);
+    A = decayed(f.p[i], A);
   }
   if (!serial) {
 #pragma unroll
     for (int i = kWarpTokens - 1; i >= 0; --i) {
-      float d[CH];
-      word(ds, i, d);
-      if (!PLAIN && ((ends >> i) & 1u)) joins(i, d);
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        R[c] = (!PLAIN && ((breaks >> i) & 1u)) ? 0.f : scan_mul(p[i][c], d[c] + R[c]);
+      Vec<CH> d = rows.template at<2>(i);
+      if (!PLAIN && ((f.ends >> i) & 1u)) d = d + joins_at(f, a, i, ch, on);
+      R = decayed(f.p[i], d + R);
+      if (!PLAIN && ((f.breaks >> i) & 1u)) R = vec<CH>(0.f);
     }
   }
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    sh.maps[warp][lane * CH + c][0] = A[c];
-    sh.maps[warp][lane * CH + c][1] = B[c];
-    sh.back[warp][lane * CH + c] = R[c];
-  }
-  if (!PLAIN && lane == 0) sh.reset[warp] = breaks != 0;
-  scan_sync();
-  // h before the warp's tokens, then before each of them
-  {
-    float h[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) h[c] = hin[c];
-    for (int q = 0; q < warp; ++q) {
-      const bool r = !PLAIN && sh.reset[q];
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        const float qb = sh.maps[q][lane * CH + c][1];
-        h[c] = r ? qb : fmaf(sh.maps[q][lane * CH + c][0], h[c], qb);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kWarpTokens; ++i) {
-      float x[CH];
-      word(xs, i, x);
-#pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        if (PLAIN || !((breaks >> i) & 1u)) before[i][c] = h[c];
-        h[c] = scan_step(p[i][c], input_of<KIND>(p[i][c], x[c]), before[i][c]);
-      }
-    }
-  }
-  // the map of the warps behind this one
-  bool fixed = false;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) { A[c] = 1.f; R[c] = 0.f; }
-  auto add_warp = [&](int q) {
-    const bool r = !PLAIN && sh.reset[q];
-    fixed |= r;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const float qa = sh.maps[q][lane * CH + c][0], qr = sh.back[q][lane * CH + c];
-      R[c] = r ? qr : fmaf(qa, R[c], qr);
-      A[c] *= qa;
-    }
-  };
-  int32_t* flag = a.w.flags + (size_t)k * a.slabs + slab;
-  bool ok = true;
-  if (!serial)
-    for (int q = kScanWarps - 1; q > warp; --q) add_warp(q);
-  if (warp == 0) {
-    const bool fixed1 = fixed;
-    float A1[CH], R1[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) { A1[c] = A[c]; R1[c] = R[c]; }
-    if (!serial) add_warp(0);
-    if (is_map_bwd(info) && k % kScanGroup != 0) {
-      if (on) st_map(a.w.maps + ((size_t)k * a.C + ch) * 2, A, R);
-      publish(flag, kFlagMap);
-    }
-    float u[CH];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) u[c] = 0.f;
-    if (info & kInfoOut) {
-      const int base = k + 1 + dist;
-      ok = join_maps(u, base, -1, dist, a.w.carry + (size_t)base * a.C + ch, a.w, a.slabs, slab, a.C, ch, on, wc);
-    }
-#pragma unroll
-    for (int c = 0; c < CH; ++c) sh.in[lane * CH + c] = u[c];
-    if (!serial && ok) {
-#pragma unroll
-      for (int c = 0; c < CH; ++c) u[c] = fixed ? R[c] : fmaf(A[c], u[c], R[c]);
-      if (on) st_state(a.w.carry + (size_t)k * a.C + ch, u);
-      publish(flag, (info & kInfoBreak) ? kFlagState : kFlagAll);
-    }
-    fixed = fixed1;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) { A[c] = A1[c]; R[c] = R1[c]; }
-  }
-  if (!scan_agree(ok)) return false;
-  float u[CH];
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    u[c] = sh.in[lane * CH + c];
-    if (warp != kScanWarps - 1) u[c] = fixed ? R[c] : fmaf(A[c], u[c], R[c]);
-  }
-  for (int turn = 0; turn < (serial ? kScanWarps : 1); ++turn) {
-    if (!serial || turn == kScanWarps - 1 - warp) {
-      if (serial) {
-#pragma unroll
-        for (int c = 0; c < CH; ++c) u[c] = sh.in[lane * CH + c];
-      }
-#pragma unroll
-      for (int i = kWarpTokens - 1; i >= 0; --i) {
-        float lam[CH], x[CH], g[CH], dg[CH], dx[CH];
-        word(ds, i, lam);
-        word(xs, i, x);
-        if (KIND == TREE_GATE_LOG) word(gs, i, g);
-        if (!PLAIN && ((ends >> i) & 1u)) joins(i, lam);
-#pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          lam[c] += u[c];
-          gate_grad<KIND>(g[c], x[c], p[i][c], before[i][c], lam[c], dg[c], dx[c]);
-          u[c] = scan_mul(p[i][c], lam[c]);
-        }
-        if (on && (PLAIN || t0 + i < a.t.N)) {
-          const size_t at = (size_t)(t0 + i) * a.C + ch;
-          *reinterpret_cast<uint32_t*>(a.dgate + at) = Lane<T>::pack(dg);
-          *reinterpret_cast<uint32_t*>(a.dx + at) = Lane<T>::pack(dx);
-        }
-        if (!PLAIN && ((breaks >> i) & 1u)) {        // what this path hands to the state it started from
-          const int f = __shfl_sync(0xffffffffu, from, i), v = __shfl_sync(0xffffffffu, own, i);
-          const int sb = __shfl_sync(0xffffffffu, sib, i);
-          float r[CH];
-          ld_state_if(a.w.dnode + (size_t)sb * a.C + ch, on && sb >= 0, r);
-#pragma unroll
-          for (int c = 0; c < CH; ++c) r[c] += u[c];
-          if (on && f >= 0) st_state(a.w.dnode + (size_t)v * a.C + ch, r);
-          if (on && f == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
-#pragma unroll
-          for (int c = 0; c < CH; ++c) u[c] = 0.f;
-        }
-      }
-      if (serial) {
-        __syncwarp();
-#pragma unroll
-        for (int c = 0; c < CH; ++c) sh.in[lane * CH + c] = u[c];
-        if (warp == 0 && on) st_state(a.w.carry + (size_t)k * a.C + ch, u);
-      }
-    }
-    if (serial) scan_sync();
-  }
-  if (!PLAIN && (serial || (info & kInfoBreak))) {
-    if (!serial) scan_sync();
-    if (warp == 0) publish(flag, kFlagAll);
-  }
-  return true;
+  sh_st(sh.A[buf][warp], A);
+  sh_st(sh.B[buf][warp], B);
+  sh_st(sh.R[buf][warp], R);
+  if (lane == 0) sh.reset[buf][warp] = f.breaks != 0;
+  return ok;
 }
 
-constexpr int kFwdStages = 3, kBwdStages = 2;      // 96 KB of copies a block, two blocks an SM
+// Second half: h before every token, then the gradients from the last token to the first.
+template <typename T, int KIND, bool PLAIN, int STAGES, int CH>
+DEVI bool bwd_second(BwdTile<CH>& f, const ScanBwd<T>& a, ScanShared<STAGES>& sh, const Rows<T>& rows, int buf,
+                     uint32_t parity, int k, int slab, int info, const WaitCtl& wc) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int ch = slab * (kRowBytes / (int)sizeof(T)) + lane * CH;
+  const bool on = ch < a.C, serial = !PLAIN && (info & kInfoSerialBack);
+  const int t0 = k * TILE + warp * kWarpTokens;
+  Vec<CH> h = f.hin;
+#pragma unroll
+  for (int q = 0; q < kScanWarps - 1; ++q) {
+    if (q >= warp) break;
+    const Vec<CH> qb = sh_ld<CH>(sh.B[buf][q]);
+    h = (!PLAIN && sh.reset[buf][q]) ? qb : vfma(sh_ld<CH>(sh.A[buf][q]), h, qb);
+  }
+#pragma unroll
+  for (int i = 0; i < kWarpTokens; ++i) {
+    if (PLAIN || !((f.breaks >> i) & 1u)) f.before[i] = h;
+    h = advance<KIND>(f.p[i], rows.template at<1>(i), f.before[i]);
+  }
+  Vec<CH> A = vec<CH>(1.f), R = vec<CH>(0.f);
+  bool fixed = false;
+  if (!serial) {
+#pragma unroll
+    for (int q = kScanWarps - 1; q > 0; --q) {
+      if (q <= warp) break;
+      const bool r = !PLAIN && sh.reset[buf][q];
+      const Vec<CH> qa = sh_ld<CH>(sh.A[buf][q]), qr = sh_ld<CH>(sh.R[buf][q]);
+      R = r ? qr : vfma(qa, R, qr);
+      A = A * qa;
+      fixed |= r;
+    }
+  }
+  const bool ok = mbar_wait_warp(&sh.ready[buf], parity, wc) && sh.in_ok[buf];
+  Vec<CH> u = sh_ld<CH>(sh.in[buf]);                 // the gradient behind the tile
+  if (!serial) {
+    if (warp < kScanWarps - 1) u = fixed ? R : vfma(A, u, R);
+  } else if (warp < kScanWarps - 1) {
+    bar_sync(kBarTurn + warp, 64);
+    u = sh_ld<CH>(sh.carry[warp + 1]);
+  }
+  if (ok) {
+#pragma unroll
+    for (int i = kWarpTokens - 1; i >= 0; --i) {
+      Vec<CH> lam = rows.template at<2>(i) + u;
+      if (!PLAIN && ((f.ends >> i) & 1u)) lam = lam + joins_at(f, a, i, ch, on);
+      const Vec<CH> p = f.p[i];
+      u = decayed(p, lam);
+      Vec<CH> dx, dg;
+      if (KIND == TREE_GATE_SIGMOID) {
+        Vec<CH> m, s;                                // the smaller of a and 1 - a; 1 - a
+#pragma unroll
+        for (int c = 0; c < CH; ++c) m.v[c] = fabsf(p.v[c]);
+        s = pick(p, m, vec<CH>(1.f) - m);
+        dx = lam * s;
+        dg = lam * (vfma(-m, m, m) * (f.before[i] - rows.template at<1>(i)));
+      } else {
+        dx = lam;
+        dg = u * f.before[i];
+        const Vec<CH> g = rows.template at<0>(i);
+#pragma unroll
+        for (int c = 0; c < CH; ++c) dg.v[c] = g.v[c] > 0.f ? 0.f : dg.v[c];
+      }
+      if (on && (PLAIN || t0 + i < a.t.N)) {
+        const size_t at = (size_t)(t0 + i) * a.C + ch;
+        *reinterpret_cast<uint32_t*>(a.dgate + at) = Lane<T>::pack(dg);
+        *reinterpret_cast<uint32_t*>(a.dx + at) = Lane<T>::pack(dx);
+      }
+      if (!PLAIN && ((f.breaks >> i) & 1u)) {        // what this path hands to the state it started from
+        const int n = __shfl_sync(0xffffffffu, f.from, i), v = __shfl_sync(0xffffffffu, f.own, i);
+        const int sb = __shfl_sync(0xffffffffu, f.sib, i);
+        const Vec<CH> later = ld_state_if(a.w.dnode + (size_t)sb * a.C + ch, on && sb >= 0, u);
+        if (on && n >= 0) st_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
+        if (on && n == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
+        u = vec<CH>(0.f);
+      }
+    }
+  }
+  if (PLAIN) return ok;
+  int32_t* flag = a.w.flags + (size_t)k * a.slabs + slab;
+  if (serial) {
+    if (warp > 0) {
+      sh_st(sh.carry[warp], u);
+      bar_arrive(kBarTurn + warp - 1, 64);
+    } else if (ok) {
+      if (on) hand_state(a.w.carry + (size_t)k * a.C + ch, u);
+      publish(flag);
+    }
+  } else if (info & kInfoBreak) {
+    bar_sync(kBarDone, kComputeThreads);
+    if (warp == 0 && ok) publish(flag);
+  }
+  return ok;
+}
+
+constexpr int kFwdStages = 2, kBwdStages = 2;
 constexpr int scan_smem(int stages, int arrays) { return stages * arrays * kBoxBytes + 1024; }
 
 DEVI uint8_t* scan_align(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
@@ -822,42 +975,59 @@ DEVI void scan_init(ScanShared<STAGES>& sh) {
     sh.abort_flag = 0;
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&sh.full[s], 2);                   // the copies' announcement, and what tile it is
-      mbar_init(&sh.empty[s], kScanWarps);
+      mbar_init(&sh.empty[s], kScanWarps + 1);     // the compute warps and the joining warp
     }
+    mbar_init(&sh.ready[0], 1);
+    mbar_init(&sh.ready[1], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
 }
 
+// Warps 0-7 compute, 8 loads, 9 joins.  The three agree once a tile (kBarMaps) whether all goes well; after a
+// wait that gave up they leave together there.
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kScanThreads, 2) k_scan_fwd(const __grid_constant__ CUtensorMap tm_gate,
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const ScanFwd<T> a) {
+  constexpr int CH = Lane<T>::CH, SLAB = kRowBytes / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScanShared<kFwdStages> sh;
   uint8_t* stages = scan_align(smem_raw);
   scan_init(sh);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  if (threadIdx.x >= 32 * kScanWarps) {
+  const int warp = threadIdx.x >> 5;
+  if (warp == kScanWarps) {
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
-    scan_loader<true>(sh, stages, tm, a.w, a.tiles, a.slabs, kRowBytes / (int)sizeof(T), TILE * a.row_bytes, wc);
+    scan_loader<true>(sh, stages, tm, a.w, a.tiles, a.slabs, SLAB, TILE * a.row_bytes, wc);
     return;
   }
+  bool ok = true;
+  if (warp == kScanWarps + 1) {
+    for (int i = 0; scan_join<true, CH>(sh, i, a.w, a.C, a.tiles, a.slabs, a.states + (size_t)a.t.n_nodes * a.C, SLAB,
+                                        wc, ok);
+         ++i) {
+    }
+    return;
+  }
+  FwdTile<CH> f;
   for (int i = 0;; ++i) {
-    const int s = i % kFwdStages;
-    bool ok = scan_agree(mbar_wait(&sh.full[s], (i / kFwdStages) & 1, wc));
-    if (!ok) break;
-    const int k = sh.tile[s], slab = sh.slab[s], info = sh.info[s], dist = sh.dist[s];
-    if (k < 0) break;
+    const int s = i % kFwdStages, buf = i & 1;
+    ok = mbar_wait_warp(&sh.full[s], (i / kFwdStages) & 1, wc) && ok;
+    int k = -1, slab = 0, info = 0;
+    if (ok) { k = sh.tile[s]; slab = sh.slab[s]; info = sh.info[s]; }
+    const bool plain = !(info & (kInfoBreak | kInfoEnd)) && (k + 1) * (int64_t)TILE <= a.t.N;
     const uint8_t* stage = stages + (size_t)s * 2 * kBoxBytes;
-    if (!(info & (kInfoBreak | kInfoEnd)) && (k + 1) * (int64_t)TILE <= a.t.N)
-      ok = scan_tile_fwd<T, KIND, true>(a, sh, stage, &sh.empty[s], k, slab, info, dist, wc);
-    else
-      ok = scan_tile_fwd<T, KIND, false>(a, sh, stage, &sh.empty[s], k, slab, info, dist, wc);
-    if (!ok) {
+    if (k >= 0)
+      ok = plain ? fwd_first<T, KIND, true>(f, a, sh, stage, &sh.empty[s], buf, k, slab, wc)
+                 : fwd_first<T, KIND, false>(f, a, sh, stage, &sh.empty[s], buf, k, slab, wc);
+    if (!bar_agree(kBarMaps, kMapThreads, ok)) {
       sh.abort_flag = 1;                           // the loading warp stops too
       break;
     }
+    if (k < 0) break;
+    ok = plain ? fwd_second<T, true>(f, a, sh, buf, (i >> 1) & 1, k, slab, info, wc)
+               : fwd_second<T, false>(f, a, sh, buf, (i >> 1) & 1, k, slab, info, wc);
   }
 }
 
@@ -866,33 +1036,48 @@ __global__ void __launch_bounds__(kScanThreads, 2) k_scan_bwd(const __grid_const
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const __grid_constant__ CUtensorMap tm_dy,
                                                               const ScanBwd<T> a) {
+  constexpr int CH = Lane<T>::CH, SLAB = kRowBytes / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScanShared<kBwdStages> sh;
   uint8_t* stages = scan_align(smem_raw);
   scan_init(sh);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  if (threadIdx.x >= 32 * kScanWarps) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == kScanWarps) {
     const CUtensorMap* tm[3] = {&tm_gate, &tm_x, &tm_dy};
-    scan_loader<false>(sh, stages, tm, a.w, a.tiles, a.slabs, kRowBytes / (int)sizeof(T), TILE * a.row_bytes, wc);
+    scan_loader<false>(sh, stages, tm, a.w, a.tiles, a.slabs, SLAB, TILE * a.row_bytes, wc);
     return;
   }
+  bool ok = true;
+  if (warp == kScanWarps + 1) {
+    for (int i = 0; scan_join<false, CH>(sh, i, a.w, a.C, a.tiles, a.slabs, a.w.carry, SLAB, wc, ok); ++i) {
+    }
+    return;
+  }
+  BwdTile<CH> f;
   for (int i = 0;; ++i) {
-    const int s = i % kBwdStages;
-    bool ok = scan_agree(mbar_wait(&sh.full[s], (i / kBwdStages) & 1, wc));
-    if (!ok) break;
-    const int k = sh.tile[s], slab = sh.slab[s], info = sh.info[s], dist = sh.dist[s];
-    if (k < 0) break;
-    const uint8_t* stage = stages + (size_t)s * 3 * kBoxBytes;
+    const int s = i % kBwdStages, buf = i & 1;
+    ok = mbar_wait_warp(&sh.full[s], (i / kBwdStages) & 1, wc) && ok;
+    int k = -1, slab = 0, info = 0;
+    if (ok) { k = sh.tile[s]; slab = sh.slab[s]; info = sh.info[s]; }
     const bool plain = !(info & (kInfoBreak | kInfoSource)) && !((info & kInfoEnd) && a.d_final) &&
                        (k + 1) * (int64_t)TILE <= a.t.N;
-    if (plain) ok = scan_tile_bwd<T, KIND, true>(a, sh, stage, k, slab, info, dist, wc);
-    else ok = scan_tile_bwd<T, KIND, false>(a, sh, stage, k, slab, info, dist, wc);
-    if (!ok) {
+    const bool on = slab * SLAB + lane * CH < a.C;
+    const Rows<T> rows{stages + (size_t)s * 3 * kBoxBytes + (size_t)(warp * kWarpTokens) * a.row_bytes +
+                           (on ? lane * 4 : 0),
+                       a.row_bytes};
+    if (k >= 0)
+      ok = plain ? bwd_first<T, KIND, true>(f, a, sh, rows, buf, k, slab, info, wc)
+                 : bwd_first<T, KIND, false>(f, a, sh, rows, buf, k, slab, info, wc);
+    if (!bar_agree(kBarMaps, kMapThreads, ok)) {
       sh.abort_flag = 1;
       break;
     }
+    if (k < 0) break;
+    ok = plain ? bwd_second<T, KIND, true>(f, a, sh, rows, buf, (i >> 1) & 1, k, slab, info, wc)
+               : bwd_second<T, KIND, false>(f, a, sh, rows, buf, (i >> 1) & 1, k, slab, info, wc);
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.empty[s]);
+    if (lane == 0) mbar_arrive(&sh.empty[s]);
   }
 }
 
@@ -943,7 +1128,7 @@ int scan_args(const tree_plan_t* plan, const int32_t* parent, const int32_t* nod
   int rc = plan_ok(plan);
   if (rc) return rc;
   if (!plan->tok_node || !plan->tok_start || !plan->sub_end || !parent || !node_len) return TREE_ERR_ARG;
-  if (plan->n_nodes <= 0 || plan->n_nodes >= kFromTile || C <= 0 || C % 8 != 0) return TREE_ERR_SHAPE;
+  if (plan->n_nodes <= 0 || C <= 0 || C % 8 != 0) return TREE_ERR_SHAPE;
   if ((dtype != TREE_BF16 && dtype != TREE_F32) || (kind != TREE_GATE_SIGMOID && kind != TREE_GATE_LOG))
     return TREE_ERR_SHAPE;
   return TREE_OK;
@@ -972,6 +1157,9 @@ int scan_grid(Kern kern, int smem, int64_t units, unsigned* blocks) {
   return rc;
 }
 
+// 12 bytes a channel are marked empty for each tile: a block for 1024 channels
+dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (unsigned)((C + 1023) / 1024)); }
+
 template <typename T, int KIND>
 int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, cudaStream_t s) {
   constexpr int smem = scan_smem(kFwdStages, 2);
@@ -999,7 +1187,7 @@ int scan_fwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<(unsigned)t.n_tiles, TILE, 0, s>>>(t, w, slabs, C, 0, states);
+  k_scan_prepare<<<prepare_grid(t, C), TILE, 0, s>>>(t, w, slabs, C, 0, states, states + (size_t)t.n_nodes * C);
   const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, t.n_tiles,
                      std::min(C * (int)sizeof(T), kRowBytes), status, wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_fwd<T, TREE_GATE_SIGMOID>(a, tg, tx, s)
@@ -1016,7 +1204,7 @@ int scan_bwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (!rc) rc = scan_map<T>(&td, dy, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<(unsigned)t.n_tiles, TILE, 0, s>>>(t, w, slabs, C, 1, d_init);
+  k_scan_prepare<<<prepare_grid(t, C), TILE, 0, s>>>(t, w, slabs, C, 1, d_init, w.carry);
   const ScanBwd<T> a{init, states, d_final, static_cast<T*>(dgate), static_cast<T*>(dx), d_init, t, w, C, slabs,
                      t.n_tiles, std::min(C * (int)sizeof(T), kRowBytes), status, wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_bwd<T, TREE_GATE_SIGMOID>(a, tg, tx, td, s)
