@@ -456,6 +456,12 @@ struct ScanBack {
   alignas(16) float before[kScanWarps][4][64];     // h before every fourth token, where it cannot stay in registers
 };
 
+// Forward: the states behind nodes that end in the tile at hand, one for every four tokens (the last that came).
+struct ScanEnds {
+  int token[TILE / 4];                             // which token's
+  alignas(16) float state[TILE / 4][64];
+};
+
 constexpr int kSlots = 3, kPlanes = 4;             // 192 KB: a block an SM
 
 template <typename T>
@@ -599,6 +605,12 @@ struct Rows {
     word(1, i) = B.v[0];
     if constexpr (CH == 2) *reinterpret_cast<float2*>(pair + i * 2 * kRow) = make_float2(A.v[1], B.v[1]);
   }
+  DEVI Vec<CH> constant(int i) const {               // B alone
+    Vec<CH> B;
+    B.v[0] = word(1, i);
+    if constexpr (CH == 2) B.v[1] = reinterpret_cast<const float2*>(pair + i * 2 * kRow)->y;
+    return B;
+  }
   DEVI Vec<CH> mapped(int i, Vec<CH> h) const {      // the token's map of the state before the warp
     Vec<CH> A, B;
     A.v[0] = word(0, i);
@@ -727,30 +739,35 @@ DEVI void fwd_map(ScanShared<kSlots>& sh, uint8_t* slots, int group, int warp, c
   }
 }
 
-// Forward, a warp whose 16 tokens hold breaks.  Their maps do not reach across a break, so it takes g and x
-// from global memory and steps through the tokens, four at a time with their loads in flight together (a
-// rolled loop: this is rare, and straight-line code for it would be fetched anew each time).
+// Forward, a warp whose 16 tokens hold breaks: the mapping warps' maps do not reach across one.  (Its loops are
+// rolled: this is rare, and straight-line code for it would be fetched anew each time.)
 template <typename T, int KIND>
 struct FwdBreaks {
   static constexpr int CH = Lane<T>::CH;
   const ScanFwd<T>& a;
-  int t0, ch;
+  const Rows<T>& rows;
+  ScanEnds& kept;
+  int k, t0, ch;
   bool on;
   int from, end;                           // per lane q < 16: link of token t0 + q, its node if it is the node's last
-  uint32_t breaks, ends;
-  // From token q0 on; h: the state before it (a break at q0 replaces it).  Returns the state behind token 15.
-  DEVI Vec<CH> walk(Vec<CH> h, int q0, bool write) const {
+  uint32_t breaks, ends, reset;            // a bit a token; reset: breaks that start from outside the tile
+  // New maps for the 16 tokens, from g and x in global memory, four at a time with their loads in flight
+  // together.  Behind a break they start anew: from outside the tile with the state itself, as a constant in B;
+  // from a node of this tile as maps of that node's state, which is not known yet.
+  DEVI Vec<CH> remap(Vec<CH>& A) const {
+    Vec<CH> B = vec<CH>(0.f);
+    A = vec<CH>(1.f);
 #pragma unroll 1
-    for (int g = q0 & ~3; g < kWarpTokens; g += 4) {
+    for (int g = 0; g < kWarpTokens; g += 4) {
       Vec<CH> s[4];
       uint32_t gw[4], xw[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int n = __shfl_sync(0xffffffffu, from, g + q);
-        const bool brk = (breaks >> (g + q)) & 1u;
+        const bool start = (reset >> (g + q)) & 1u;
         const float* row = n >= 0 ? a.states + (size_t)n * a.C
-                                  : (a.init && brk ? a.init + (size_t)a.t.tok_node[t0 + g + q] * a.C : nullptr);
-        s[q] = ld_state_if(row + ch, on && row && brk && g + q >= q0, h);
+                                  : (a.init && start ? a.init + (size_t)a.t.tok_node[t0 + g + q] * a.C : nullptr);
+        s[q] = ld_state_if(row + ch, on && row && start, B);
         const bool live = on && t0 + g + q < a.t.N;
         const size_t at = (size_t)(t0 + g + q) * a.C + ch;
         gw[q] = live ? *reinterpret_cast<const uint32_t*>(a.gate + at) : 0u;
@@ -758,47 +775,85 @@ struct FwdBreaks {
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (g + q < q0) continue;
         if ((breaks >> (g + q)) & 1u) {
-          h = s[q];
-          // the start may be a node that ended within these four tokens: then its row is only now there
-          const int n = __shfl_sync(0xffffffffu, from, g + q);
-          if (n >= 0 && __any_sync(0xffffffffu, end == n)) h = ld_state_if(a.states + (size_t)n * a.C + ch, on, h);
+          A = vec<CH>(1.f);
+          B = ((reset >> (g + q)) & 1u) ? s[q] : vec<CH>(0.f);
         }
-        h = advance<KIND>(gate_of<KIND>(Lane<T>::unpack(gw[q])), Lane<T>::unpack(xw[q]), h);
-        if (write && on && t0 + g + q < a.t.N)
-          *reinterpret_cast<uint32_t*>(a.y + (size_t)(t0 + g + q) * a.C + ch) = Lane<T>::pack(h);
-        if (write && ((ends >> (g + q)) & 1u)) {
-          const int e = __shfl_sync(0xffffffffu, end, g + q);
-          if (on) st_state(a.states + (size_t)e * a.C + ch, h);
-        }
+        const Vec<CH> p = gate_of<KIND>(Lane<T>::unpack(gw[q]));
+        B = advance<KIND>(p, Lane<T>::unpack(xw[q]), B);
+        A = decayed(p, A);
+        rows.set_map(g + q, A, B);
       }
     }
-    return h;
+    return B;
+  }
+  // The state that the run of tokens behind the break at q starts from, a node of this tile's.
+  DEVI Vec<CH> source(int q) const {
+    const int n = __shfl_sync(0xffffffffu, from, q);
+    const int tok = a.t.tok_start[n] + a.t.node_len[n] - 1 - k * TILE, slot = tok / 4;
+    if (kept.token[slot] == tok) return sh_ld<CH>(kept.state[slot]);
+    return ld_state_if(a.states + (size_t)n * a.C + ch, on, Vec<CH>());     // another end has taken its place
+  }
+  DEVI void keep(int q, Vec<CH> v) const {   // the state of the node that ends at q
+    const int e = __shfl_sync(0xffffffffu, end, q), tok = t0 + q - k * TILE, slot = tok / 4;
+    if (on) st_state(a.states + (size_t)e * a.C + ch, v);
+    sh_st(kept.state[slot], v);
+    if ((threadIdx.x & 31) == 0) kept.token[slot] = tok;
+    __syncwarp();
+  }
+  // Through the tokens at which something happens; h: the state before the warp.  Returns the state behind it.
+  DEVI Vec<CH> pass(Vec<CH> h, bool keeping) const {
+    bool set = false;                        // the run's states are in B already
+    for (uint32_t m = (breaks & ~reset) | reset | (keeping ? ends : 0u); m; m &= m - 1) {
+      const int q = __ffs(m) - 1;
+      if ((breaks >> q) & 1u) {
+        set = (reset >> q) & 1u;
+        if (!set) h = source(q);
+      }
+      if ((ends >> q) & 1u) {
+        const Vec<CH> v = set ? rows.constant(q) : rows.mapped(q, h);
+        if (keeping) keep(q, v);
+      }
+    }
+    return set ? rows.constant(kWarpTokens - 1) : rows.mapped(kWarpTokens - 1, h);
+  }
+  DEVI void write(Vec<CH> h) const {
+    bool set = false;
+#pragma unroll 1
+    for (int q = 0; q < kWarpTokens; ++q) {
+      if ((breaks >> q) & 1u) {
+        set = (reset >> q) & 1u;
+        if (!set) h = source(q);
+      }
+      const Vec<CH> v = set ? rows.constant(q) : rows.mapped(q, h);
+      if (on && t0 + q < a.t.N) *reinterpret_cast<uint32_t*>(a.y + (size_t)(t0 + q) * a.C + ch) = Lane<T>::pack(v);
+    }
   }
 };
 
 // The walking warps, forward.  Returns where a wait gave up or the tiles have ended.
 template <typename T, int KIND>
-DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
+DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, ScanEnds& kept, uint8_t* slots, int warp,
+                   const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
-  uint32_t n_own = 0, n_turn = 0;          // uses of the walking warps' barriers so far
+  uint32_t n_own = 0, n_turn = 0;                      // uses of the walking warps' barriers so far
   Tile t;
   for (int i = 0; next_tile(sh, i, t, wc) && tile_info(sh, t, wc); ++i) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;          // the lane's first channel
     const int t0 = t.k * TILE + warp * kWarpTokens;
-    FwdBreaks<T, KIND> f{a, t0, ch, ch < a.C, kLinkChain, -1, 0u, 0u};
+    FwdBreaks<T, KIND> f{a, rows, kept, t.k, t0, ch, ch < a.C, kLinkChain, -1, 0u, 0u, 0u};
     const bool serial = t.info & kInfoSerial;
     if (t.info & (kInfoBreak | kInfoEnd)) {
-      bool ok = true;
+      bool ok = true, tile = false;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
         f.from = a.w.link[t0 + lane];
         f.end = a.w.end[t0 + lane];
         if (f.from >= 0) {
           const int ts = (a.t.tok_start[f.from] + a.t.node_len[f.from] - 1) / TILE;
-          if (ts != t.k) ok = wait_rows(a.w.flags + (size_t)ts * a.slabs + t.slab, wc, a.w.ctl + 2);
+          tile = ts == t.k;
+          if (!tile) ok = wait_rows(a.w.flags + (size_t)ts * a.slabs + t.slab, wc, a.w.ctl + 2);
         }
       }
       if (!__all_sync(0xffffffffu, ok)) {
@@ -807,20 +862,24 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, uint8_t* slots, 
       }
       f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
       f.ends = __ballot_sync(0xffffffffu, f.end >= 0);
+      f.reset = f.breaks & ~__ballot_sync(0xffffffffu, tile);
     }
     if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
     if (t.info & kInfoBreak) {
-      if (!serial) {
-        if (f.breaks) sh_st(sh.B[t.s][warp], f.walk(vec<CH>(0.f), 31 - __clz(f.breaks), false));
-        if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
+      if (f.breaks) {
+        Vec<CH> A;
+        const Vec<CH> B = f.remap(A);
+        sh_st(sh.B[t.s][warp], B);                     // (a tile whose warps go one by one has no use for it)
       }
+      if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
+      if (serial && lane < TILE / 4 / kScanWarps) kept.token[warp * (TILE / 4 / kScanWarps) + lane] = -1;
       // All maps are there; and no warp is a tile ahead, where its next turn would overtake this one's.
       warp_arrive(&sh.own);
       if (!wait_phase(&sh.own, n_own & 1, wc)) return;
       ++n_own;
     }
     // The state before the warp: from the maps of the warps before it; where a break starts from a node that
-    // ends in this very tile, from the warp before it, which has then written its nodes' rows.
+    // ends in this very tile, from the warp before it, which has then kept its nodes' states.
     Vec<CH> h;
     if (!serial) {
       Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
@@ -842,27 +901,22 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, uint8_t* slots, 
       ++n_turn;
       h = sh_ld<CH>(warp > 0 ? sh.carry[warp - 1] : sh.in[t.s]);
     }
-    Vec<CH> last = h;                                  // the state behind the warp
-    if (f.breaks) {
-      last = f.walk(h, 0, true);
-    } else {
-      for (uint32_t m = f.ends; m; m &= m - 1) {
-        const int q = __ffs(m) - 1, e = __shfl_sync(0xffffffffu, f.end, q);
-        const Vec<CH> v = rows.mapped(q, h);
-        if (f.on) st_state(a.states + (size_t)e * a.C + ch, v);
-      }
-      if (t.info & kInfoBreak) last = vfma(sh_ld<CH>(sh.A[t.s][warp]), h, sh_ld<CH>(sh.B[t.s][warp]));
-    }
+    // first what others wait for: nodes' states, and the state behind the warp
     int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
-    if (serial && warp < kScanWarps - 1) {
-      sh_st(sh.carry[warp], last);
-      warp_arrive(&sh.turn[warp + 1]);
+    if (t.info & (kInfoBreak | kInfoEnd)) {
+      const Vec<CH> last = f.pass(h, true);
+      if (serial && warp < kScanWarps - 1) {
+        sh_st(sh.carry[warp], last);
+        warp_arrive(&sh.turn[warp + 1]);
+      }
+      if ((t.info & kInfoBreak) && warp == kScanWarps - 1) {
+        if (f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, last);
+        if (serial) publish(flag);
+      }
     }
-    if ((t.info & kInfoBreak) && warp == kScanWarps - 1) {
-      if (f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, last);
-      if (serial) publish(flag);
-    }
-    if (!f.breaks) {
+    if (f.breaks) {
+      f.write(h);
+    } else {
       T* y = a.y + (size_t)t0 * a.C + ch;
       const int rest = f.on ? a.t.N - t0 : 0;          // tokens to write
 #pragma unroll 4
@@ -918,12 +972,14 @@ struct BwdBreaks {
   uint32_t breaks, joins;
   // h before four tokens from g on; h: before token g, and on return behind the four
   DEVI void befores(int g, Vec<CH>& h, Vec<CH> (&b)[4]) const {
+    if ((breaks >> g) & 15u) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = __shfl_sync(0xffffffffu, from, g + q), v = __shfl_sync(0xffffffffu, own, g + q);
-      const bool brk = (breaks >> (g + q)) & 1u;
-      const float* row = n >= 0 ? a.states + (size_t)n * a.C : (a.init && brk ? a.init + (size_t)v * a.C : nullptr);
-      b[q] = ld_state_if(row + ch, on && row && brk, h);
+      for (int q = 0; q < 4; ++q) {
+        const int n = __shfl_sync(0xffffffffu, from, g + q), v = __shfl_sync(0xffffffffu, own, g + q);
+        const bool brk = (breaks >> (g + q)) & 1u;
+        const float* row = n >= 0 ? a.states + (size_t)n * a.C : (a.init && brk ? a.init + (size_t)v * a.C : nullptr);
+        b[q] = ld_state_if(row + ch, on && row && brk, h);
+      }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -934,6 +990,9 @@ struct BwdBreaks {
   // dy of four tokens and what joins it: kid: the next node that starts from this one's state, with those behind
   // it; end: the node's own final state
   DEVI void sums(int g, Vec<CH> (&d)[4]) const {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) d[q] = rows.get(2, g + q);
+    if (!((joins >> g) & 15u)) return;
     Vec<CH> f[4], k[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -942,7 +1001,7 @@ struct BwdBreaks {
       k[q] = ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on && kd >= 0, d[q]);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) d[q] = rows.get(2, g + q) + (f[q] + k[q]);
+    for (int q = 0; q < 4; ++q) d[q] = d[q] + (f[q] + k[q]);
   }
 };
 
@@ -1173,6 +1232,7 @@ __global__ void __launch_bounds__(scan_threads(kFwdGroups), 1) k_scan_fwd(const 
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
   __shared__ ScanShared<kSlots> sh;
+  __shared__ ScanEnds kept;
   uint8_t* slots = scan_align(smem_raw);
   scan_init(sh);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
@@ -1181,7 +1241,7 @@ __global__ void __launch_bounds__(scan_threads(kFwdGroups), 1) k_scan_fwd(const 
   if (warp < WALK) {
     fwd_map<T, KIND, kFwdGroups>(sh, slots, warp / kScanWarps, warp % kScanWarps, wc);
   } else if (warp < LOAD) {
-    fwd_walk<T, KIND>(a, sh, slots, warp - WALK, wc);
+    fwd_walk<T, KIND>(a, sh, kept, slots, warp - WALK, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
     scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, false, wc);
