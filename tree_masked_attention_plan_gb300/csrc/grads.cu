@@ -36,25 +36,34 @@ struct GradList {
   int n, chunks;
 };
 
-// Squares are summed in fp32 within one 16-byte vector and in fp64 across vectors.  An fp32
-// square is out of range or inexact where the value is above 2^60 or below 2^-50: a vector whose
-// largest value lies there is squared in fp64.
-template <int CNT>
-DEVI double sum_squares(const float (&v)[CNT]) {
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < CNT; ++i) m = fmaxf(m, fabsf(v[i]));
-  if (m > 0x1p60f || (m < 0x1p-50f && m > 0.f)) {
-    double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < CNT; ++i) s += (double)v[i] * (double)v[i];
-    return s;
+// A thread's sum of squares.  fp64 additions are rare on this GPU (two a clock and SM: one for every 16-byte
+// vector made the norm of 528M fp32 elements take 2.4 ms instead of 0.3), so a vector's squares are summed in
+// fp32 and the vectors' sums in a pair of fp32 that holds what each addition rounds away.  A vector with a value
+// above 2^40 or with none above 2^-50, whose squares fp32 may not hold, is squared and summed in fp64.
+struct Squares {
+  float s = 0.f, c = 0.f;
+  double rest = 0.0;
+  DEVI void add(float v) {                    // s + c += v: s takes the rounded sum, c the rounding
+    const float t = s + v, z = t - s;
+    c += (s - (t - z)) + (v - z);
+    s = t;
   }
-  float s = 0.f;
+  template <int CNT>
+  DEVI void vec(const float (&v)[CNT]) {
+    float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < CNT; ++i) s = fmaf(v[i], v[i], s);
-  return (double)s;
-}
+    for (int i = 0; i < CNT; ++i) m = fmaxf(m, fabsf(v[i]));
+    if (m > 0x1p40f || (m < 0x1p-50f && m > 0.f)) {
+#pragma unroll
+      for (int i = 0; i < CNT; ++i) rest += (double)v[i] * (double)v[i];
+    } else {
+      float q = 0.f;
+#pragma unroll
+      for (int i = 0; i < CNT; ++i) q = fmaf(v[i], v[i], q);
+      add(q);
+    }
+  }
+};
 
 DEVI void load_vec(const uint8_t* p, float (&v)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
@@ -94,27 +103,55 @@ DEVI int64_t head_elems(const uint8_t* p, int64_t n) {
   return h < n ? h : n;
 }
 
-// the sum of squares of one chunk's n elements at p, this thread's share
+// one chunk's n elements at p, this thread's share
 template <int CNT>
-DEVI double chunk_squares(const uint8_t* p, int64_t n) {
+DEVI void chunk_squares(const uint8_t* p, int64_t n, Squares& sq) {
   constexpr int ES = 16 / CNT;
-  double s = 0.0;
   const int64_t head = head_elems<CNT>(p, n);
   const int nvec = static_cast<int>((n - head) / CNT);
   const uint8_t* pv = p + head * ES;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < nvec; i += kGradThreads) {
+  int i = threadIdx.x;
+  for (; i + 3 * kGradThreads < nvec; i += 4 * kGradThreads) {       // four loads in flight
+    float v[4][CNT];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load_vec(pv + (size_t)(i + q * kGradThreads) * 16, v[q]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sq.vec(v[q]);
+  }
+  for (; i < nvec; i += kGradThreads) {
     float v[CNT];
     load_vec(pv + (size_t)i * 16, v);
-    s += sum_squares(v);
+    sq.vec(v);
   }
   const int64_t tail = head + (int64_t)nvec * CNT;
   const int64_t rest = head + (n - tail);          // single elements: before and behind the vectors
   if (threadIdx.x < rest) {
     const int64_t j = threadIdx.x < head ? threadIdx.x : tail + (threadIdx.x - head);
     const float one[1] = {load_one<CNT>(p + j * ES)};
-    s += sum_squares(one);
+    sq.vec(one);
   }
+}
+
+// the block's sum, in thread 0
+DEVI double block_squares(Squares& q, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float s = __shfl_xor_sync(0xffffffffu, q.s, o), c = __shfl_xor_sync(0xffffffffu, q.c, o);
+    q.add(s);
+    q.c += c;
+  }
+  double v = (double)q.s + (double)q.c;
+  if (__any_sync(0xffffffffu, q.rest != 0.0)) {    // (NaN: the sum is NaN)
+    double r = q.rest;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    v += r;
+  }
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < kGradThreads / 32; ++i) s += red[i];
   return s;
 }
 
@@ -126,7 +163,6 @@ DEVI double block_sum(double v, double* red) {
   double s = 0.0;
 #pragma unroll
   for (int i = 0; i < kGradThreads / 32; ++i) s += red[i];
-  __syncthreads();
   return s;
 }
 
@@ -145,15 +181,15 @@ DEVI int entry_of(const GradList<MAX>& L, int c) {
 template <int MAX>
 __global__ void __launch_bounds__(kGradThreads) k_grad_squares(const __grid_constant__ GradList<MAX> L, double* part) {
   __shared__ double red[kGradThreads / 32];
-  double s = 0.0;
+  Squares sq;
   for (int c = blockIdx.x; c < L.chunks; c += gridDim.x) {
     const GradEntry& e = L.e[entry_of(L, c)];
     const int64_t at = (int64_t)(c - e.first) * kChunk;
     const int64_t n = min((int64_t)kChunk, e.numel - at);
-    if (e.f32) s += chunk_squares<4>(e.src + at * 4, n);
-    else s += chunk_squares<8>(e.src + at * 2, n);
+    if (e.f32) chunk_squares<4>(e.src + at * 4, n, sq);
+    else chunk_squares<8>(e.src + at * 2, n, sq);
   }
-  s = block_sum(s, red);
+  const double s = block_squares(sq, red);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
@@ -186,19 +222,28 @@ DEVI void chunk_scale(const uint8_t* p, uint8_t* o, int64_t n, float c) {
   }
   const int64_t head = head_elems<CNT>(p, n);
   const int nvec = static_cast<int>((n - head) / CNT);
-#pragma unroll 4
-  for (int i = threadIdx.x; i < nvec; i += kGradThreads) {
-    const size_t at = head * ES + (size_t)i * 16;
+  auto out = [&](uint8_t* to, uint4 w) {
     if (CLIP) {
       float v[CNT];
-      load_vec(p + at, v);
+      load_vec(reinterpret_cast<const uint8_t*>(&w), v);
 #pragma unroll
       for (int e = 0; e < CNT; ++e) v[e] *= c;
-      store_vec(o + at, v);
+      store_vec(to, v);
     } else {
-      *reinterpret_cast<uint4*>(o + at) = *reinterpret_cast<const uint4*>(p + at);
+      *reinterpret_cast<uint4*>(to) = w;
     }
+  };
+  const uint8_t* pv = p + head * ES;
+  uint8_t* ov = o + head * ES;
+  int i = threadIdx.x;
+  for (; i + 3 * kGradThreads < nvec; i += 4 * kGradThreads) {
+    uint4 w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = *reinterpret_cast<const uint4*>(pv + (size_t)(i + q * kGradThreads) * 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) out(ov + (size_t)(i + q * kGradThreads) * 16, w[q]);
   }
+  for (; i < nvec; i += kGradThreads) out(ov + (size_t)i * 16, *reinterpret_cast<const uint4*>(pv + (size_t)i * 16));
   const int64_t tail = head + (int64_t)nvec * CNT;
   const int64_t rest = head + (n - tail);
   if (threadIdx.x < rest) one(threadIdx.x < head ? threadIdx.x : tail + (threadIdx.x - head));
