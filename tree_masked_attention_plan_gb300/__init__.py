@@ -573,51 +573,54 @@ def diag_gemm(A, B, M, N, K, a_mn, b_mn, status=None, stream=None):
     return C
 
 
-class _Launch:
-    """Makes `device` the current one and `stream` (default: the device's current one) the current stream, so
-    that what a call allocates belongs to the stream its kernels run on."""
-
-    def __init__(self, device, stream):
-        self.device = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.device is not None:
-            self.device.__enter__()
-        if self.stream is not None:
-            self.stream.__enter__()
-        return _stream()
-
-    def __exit__(self, *exc):
-        if self.stream is not None:
-            self.stream.__exit__(*exc)
-        if self.device is not None:
-            self.device.__exit__(*exc)
+def _launch(dev, stream, call):
+    """call(raw stream), with `dev` the current device and `stream` (default: the device's current one) the
+    current stream, so that what the call allocates belongs to the stream its kernels run on."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return call(torch._C._cuda_getCurrentRawStream(dev.index))
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream: expected one of {dev}, got {stream.device}")
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch._C._cuda_getCurrentRawStream(dev.index))
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
 
 
-def _need_on(device, t, shape, dtype, name):
-    """_need, and on the plan's device."""
-    _need(t, shape, dtype, name)
-    if t.device != device:
-        raise ValueError(f"{name}: expected on {device}, got {t.device}")
+def _need_on(dev, t, shape, dtype, name):
+    """_need, and on the device `dev` (checked first, all at once)."""
+    if t.device != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _need(t, shape, dtype, name)
+        raise ValueError(f"{name}: expected on {dev}, got {t.device}")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rope_axes(name, plan, pos, q, k, sections, theta, interleaved, oq, ok, stream):
-    Hq, Hkv, d = _heads(plan, q, k)
-    dev, n_axes = plan.device, len(sections)
-    for t, what in ((q, "q"), (k, "k")):
-        _need_on(dev, t, tuple(t.shape), torch.bfloat16, what)
-    _need_on(dev, pos, (n_axes, plan.n_tokens), torch.int32, "pos")
-    for t, like, what in ((oq, q, "the q output"), (ok, k, "the k output")):
-        if t is not None:
-            _need_on(dev, t, tuple(like.shape), torch.bfloat16, what)
-    sec = (_i32 * max(1, n_axes))(*[int(s) for s in sections])
-    with _Launch(dev, stream) as st:
-        oq = torch.empty_like(q) if oq is None else oq
-        ok = torch.empty_like(k) if ok is None else ok
-        _check(getattr(_lib(), name)(plan.ref(), _ptr(pos), sec, n_axes, int(bool(interleaved)), _ptr(q), _ptr(k),
-                                     _ptr(oq), _ptr(ok), Hq, Hkv, d, float(theta), st), name)
-    return oq, ok
+    N, dev, n_axes = plan.n_tokens, plan.device, len(sections)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k must be [N, heads, d]")
+    Hq, d, Hkv = q.shape[1], q.shape[2], k.shape[1]
+    bf16 = torch.bfloat16
+    _need_on(dev, q, (N, Hq, d), bf16, "q")
+    _need_on(dev, k, (N, Hkv, d), bf16, "k")
+    _need_on(dev, pos, (n_axes, N), torch.int32, "pos")
+    if oq is not None:
+        _need_on(dev, oq, q.shape, bf16, "the q output")
+    if ok is not None:
+        _need_on(dev, ok, k.shape, bf16, "the k output")
+    sec = (_i32 * max(1, n_axes))(*sections)
+
+    def call(st):
+        rq = torch.empty_like(q) if oq is None else oq
+        rk = torch.empty_like(k) if ok is None else ok
+        _check(getattr(_lib(), name)(plan.ref(), pos.data_ptr(), sec, n_axes, int(interleaved), q.data_ptr(),
+                                     k.data_ptr(), rq.data_ptr(), rk.data_ptr(), Hq, Hkv, d, theta, st), name)
+        return rq, rk
+
+    return _launch(dev, stream, call)
 
 
 def tree_rope_axes_fwd(plan: TreePlan, pos, q, k, sections, theta=10000.0, interleaved=False, qr=None, kr=None,
@@ -672,8 +675,9 @@ def _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status):
     if gate_kind not in GATES:
         raise ValueError(f"gate_kind must be one of {sorted(GATES)}")
     C, dev, n = x.shape[1], plan.device, plan.info.n_nodes
-    _need_on(dev, x, (plan.n_tokens, C), x.dtype, "x")
-    _need_on(dev, gate, (plan.n_tokens, C), x.dtype, "gate")
+    shape = (plan.n_tokens, C)
+    _need_on(dev, x, shape, x.dtype, "x")
+    _need_on(dev, gate, shape, x.dtype, "gate")
     _need_on(dev, parent, (n,), torch.int32, "parent")
     _need_on(dev, node_len, (n,), torch.int32, "node_len")
     if init is not None:
@@ -682,7 +686,7 @@ def _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status):
         _need_on(dev, status, (1,), torch.int32, "status")
     need = tree_scan_workspace(plan, C)
     if workspace is not None:
-        _need_on(dev, workspace, tuple(workspace.shape), torch.uint8, "workspace")
+        _need_on(dev, workspace, workspace.shape, torch.uint8, "workspace")
         if workspace.numel() < need:
             raise ValueError(f"workspace: {workspace.numel()} bytes, {need} needed")
     return C, dev, n, need
@@ -695,18 +699,22 @@ def tree_scan_fwd(plan: TreePlan, tree, gate, x, init=None, gate_kind="sigmoid",
     [n_nodes, C] fp32: the states that nodes without a token-holding ancestor start from.  Returns (y [N, C],
     states [n_nodes + n_tiles, C] fp32): states[v] is node v's final state, the rest is for tree_scan_bwd."""
     C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
+    rows = n + plan.n_tiles
     if y is not None:
-        _need_on(dev, y, tuple(x.shape), x.dtype, "y")
+        _need_on(dev, y, x.shape, x.dtype, "y")
     if states is not None:
-        _need_on(dev, states, (n + plan.n_tiles, C), torch.float32, "states")
-    with _Launch(dev, stream) as st:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        y = torch.empty_like(x) if y is None else y
-        states = torch.empty(n + plan.n_tiles, C, dtype=torch.float32, device=dev) if states is None else states
-        _check(_lib().tree_scan_fwd(plan.ref(), _ptr(tree[0]), _ptr(tree[1]), _ptr(gate), _ptr(x), _ptr(init), C,
-                                    _DTYPES[x.dtype], GATES[gate_kind], _ptr(workspace), _ptr(y), _ptr(states),
-                                    _ptr(status), st), "tree_scan_fwd")
-    return y, states
+        _need_on(dev, states, (rows, C), torch.float32, "states")
+
+    def call(st):
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        oy = torch.empty_like(x) if y is None else y
+        os = torch.empty((rows, C), dtype=torch.float32, device=dev) if states is None else states
+        _check(_lib().tree_scan_fwd(plan.ref(), tree[0].data_ptr(), tree[1].data_ptr(), gate.data_ptr(), x.data_ptr(),
+                                    _at(init), C, _DTYPES[x.dtype], GATES[gate_kind], ws.data_ptr(), oy.data_ptr(),
+                                    os.data_ptr(), _at(status), st), "tree_scan_fwd")
+        return oy, os
+
+    return _launch(dev, stream, call)
 
 
 def tree_scan_bwd(plan: TreePlan, tree, gate, x, states, dy, init=None, d_final=None, gate_kind="sigmoid",
@@ -715,25 +723,27 @@ def tree_scan_bwd(plan: TreePlan, tree, gate, x, states, dy, init=None, d_final=
     gradient of the nodes' final states.  Returns (dgate, dx, d_init): d_init [n_nodes, C] fp32 if init or a
     d_init to write was given, else None."""
     C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
-    _need_on(dev, dy, tuple(x.shape), x.dtype, "dy")
+    _need_on(dev, dy, x.shape, x.dtype, "dy")
     _need_on(dev, states, (n + plan.n_tiles, C), torch.float32, "states")
     for t, what in ((dgate, "dgate"), (dx, "dx")):
         if t is not None:
-            _need_on(dev, t, tuple(x.shape), x.dtype, what)
+            _need_on(dev, t, x.shape, x.dtype, what)
     for t, what in ((d_final, "d_final"), (d_init, "d_init")):
         if t is not None:
             _need_on(dev, t, (n, C), torch.float32, what)
-    with _Launch(dev, stream) as st:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
-        dgate = torch.empty_like(x) if dgate is None else dgate
-        dx = torch.empty_like(x) if dx is None else dx
-        if d_init is None and init is not None:
-            d_init = torch.empty_like(init)
-        _check(_lib().tree_scan_bwd(plan.ref(), _ptr(tree[0]), _ptr(tree[1]), _ptr(gate), _ptr(x), _ptr(init),
-                                    _ptr(states), _ptr(dy), _ptr(d_final), C, _DTYPES[x.dtype], GATES[gate_kind],
-                                    _ptr(workspace), _ptr(dgate), _ptr(dx), _ptr(d_init), _ptr(status), st),
-               "tree_scan_bwd")
-    return dgate, dx, d_init
+
+    def call(st):
+        ws = torch.empty(need, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        og = torch.empty_like(x) if dgate is None else dgate
+        ox = torch.empty_like(x) if dx is None else dx
+        oi = torch.empty_like(init) if d_init is None and init is not None else d_init
+        _check(_lib().tree_scan_bwd(plan.ref(), tree[0].data_ptr(), tree[1].data_ptr(), gate.data_ptr(), x.data_ptr(),
+                                    _at(init), states.data_ptr(), dy.data_ptr(), _at(d_final), C, _DTYPES[x.dtype],
+                                    GATES[gate_kind], ws.data_ptr(), og.data_ptr(), ox.data_ptr(), _at(oi),
+                                    _at(status), st), "tree_scan_bwd")
+        return og, ox, oi
+
+    return _launch(dev, stream, call)
 
 
 @dataclass
@@ -758,6 +768,8 @@ def tree_grad_list(grads, out=None) -> GradList:
     if len(outs) != len(grads):
         raise ValueError(f"out has {len(outs)} tensors, grads {len(grads)}")
     dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError(f"grads[0]: expected on a CUDA device, got {dev}")
     c = (GradT * len(grads))()
     for i, (g, o) in enumerate(zip(grads, outs)):
         if g.dtype not in _DTYPES:
@@ -770,28 +782,28 @@ def tree_grad_list(grads, out=None) -> GradList:
     return GradList(grads=grads, out=outs, c=c, workspace=ws, device=dev)
 
 
-def _grad_call(grads, norm, stream, call):
+def _grad_call(name, grads, norm, stream, *args):
     gl = grads if isinstance(grads, GradList) else tree_grad_list(grads)
     if norm is not None:
         _need_on(gl.device, norm, (1,), torch.float32, "norm")
-    with _Launch(gl.device, stream) as st:
-        norm = torch.empty(1, dtype=torch.float32, device=gl.device) if norm is None else norm
-        call(gl, norm, st)
-    return norm
+
+    def call(st):
+        out = torch.empty(1, dtype=torch.float32, device=gl.device) if norm is None else norm
+        _check(getattr(_lib(), name)(gl.c, len(gl.grads), *args, gl.workspace.data_ptr(), out.data_ptr(), st), name)
+        return out
+
+    return _launch(gl.device, stream, call)
 
 
 def tree_grad_norm(grads, norm=None, stream=None):
     """The global norm over a list of tensors or a GradList: fp32 [1], summed in fp64, deterministic."""
-    return _grad_call(grads, norm, stream, lambda gl, nrm, st: _check(
-        _lib().tree_grad_norm(gl.c, len(gl.grads), _ptr(gl.workspace), _ptr(nrm), st), "tree_grad_norm"))
+    return _grad_call("tree_grad_norm", grads, norm, stream)
 
 
 def tree_grad_clip(grads, max_norm, norm=None, stream=None):
     """Scale the gradients by max_norm / norm where their global norm is above max_norm, in place or into the
     GradList's out; an infinite or NaN norm leaves them as they are.  Returns the norm before, fp32 [1]."""
-    return _grad_call(grads, norm, stream, lambda gl, nrm, st: _check(
-        _lib().tree_grad_clip(gl.c, len(gl.grads), float(max_norm), _ptr(gl.workspace), _ptr(nrm), st),
-        "tree_grad_clip"))
+    return _grad_call("tree_grad_clip", grads, norm, stream, max_norm)
 
 
 __all__ += ["tree_rope_axes_fwd", "tree_rope_axes_bwd", "tree_axis_positions", "tree_scan_workspace",

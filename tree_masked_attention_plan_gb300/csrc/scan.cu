@@ -24,6 +24,7 @@
 // tokens does not lose its length to the rounding of a; the step h + (p h + b) then adds a small
 // increment to h.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 
@@ -1345,15 +1346,22 @@ int scan_map(CUtensorMap* m, const void* base, int C, int N) {
   return sizeof(T) == 2 ? make_tmap_bf16_2d(m, base, C, N, box, TILE) : make_tmap_f32_2d(m, base, C, N, box, TILE);
 }
 
-// a block an SM, or one for each unit of work
-template <typename Kern>
-int scan_grid(Kern kern, int smem, int64_t units, unsigned* blocks) {
-  int rc = record_cuda(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+// A block an SM, or one for each unit of work.  The kernel's shared memory is announced once a device.
+template <auto KERN>
+int scan_grid(int64_t units, unsigned* blocks) {
+  static std::atomic<int> sms_of[64];              // one array a kernel; 0: not announced yet
   int dev = 0, sms = 0;
-  if (!rc) rc = record_cuda(cudaGetDevice(&dev));
-  if (!rc) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+  int rc = record_cuda(cudaGetDevice(&dev));
+  if (rc) return rc;
+  if (dev < 64) sms = sms_of[dev].load(std::memory_order_acquire);
+  if (!sms) {
+    rc = record_cuda(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem));
+    if (!rc) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (rc) return rc;
+    if (dev < 64) sms_of[dev].store(sms, std::memory_order_release);
+  }
   *blocks = (unsigned)std::min<int64_t>(units, sms);
-  return rc;
+  return TREE_OK;
 }
 
 // 12 bytes a channel are marked empty for each tile: a block for 1024 channels
@@ -1361,20 +1369,18 @@ dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (
 
 template <typename T, int KIND>
 int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, cudaStream_t s) {
-  constexpr int smem = kScanSmem;
   unsigned blocks = 0;
-  const int rc = scan_grid(k_scan_fwd<T, KIND>, smem, (int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_fwd<T, KIND>>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdGroups), smem, s>>>(tg, tx, a);
+  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdGroups), kScanSmem, s>>>(tg, tx, a);
   return record_cuda(cudaGetLastError());
 }
 template <typename T, int KIND>
 int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, const CUtensorMap& td, cudaStream_t s) {
-  constexpr int smem = kScanSmem;
   unsigned blocks = 0;
-  const int rc = scan_grid(k_scan_bwd<T, KIND>, smem, (int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_bwd<T, KIND>>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdGroups), smem, s>>>(tg, tx, td, a);
+  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdGroups), kScanSmem, s>>>(tg, tx, td, a);
   return record_cuda(cudaGetLastError());
 }
 
