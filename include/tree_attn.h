@@ -368,6 +368,11 @@ enum { TREE_BF16 = 0, TREE_F32 = 1 };
  *   TREE_GATE_LOG:     a = exp(min(g, 0)), b = x   (g a log decay; no gradient where g > 0) */
 enum { TREE_GATE_SIGMOID = 0, TREE_GATE_LOG = 1 };
 
+#define TREE_SCAN_TILE 128              /* tokens between two of the states that the backward starts from */
+
+/* Rows of tree_scan_fwd's states: n_nodes + ceil(N / TREE_SCAN_TILE). */
+int64_t tree_scan_rows(const tree_plan_t* plan);
+
 /* Bytes of workspace tree_scan_fwd and tree_scan_bwd need for C channels. */
 size_t tree_scan_workspace(const tree_plan_t* plan, int C);
 
@@ -378,9 +383,9 @@ size_t tree_scan_workspace(const tree_plan_t* plan, int C);
  * token-holding ancestor starts from its row of init (fp32 [n_nodes][C], other rows are not read),
  * or from zero if init is NULL.  One-token nodes without parents are a decoding step.
  * gate, x, y: [N][C] in packed order, all of type dtype (TREE_BF16 or TREE_F32).
- * states: fp32 [n_nodes + n_tiles][C].  Row v < n_nodes receives node v's final state (zeros where
- * the node holds no tokens), row n_nodes + k the state after the last token of tile k: what the
- * backward starts from.  States are fp32 throughout; y is rounded once.  A state that becomes
+ * states: fp32 [tree_scan_rows()][C].  Row v < n_nodes receives node v's final state (zeros where the
+ * node holds no tokens); the rows behind them are for the backward (row n_nodes + k: the state after
+ * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout; y is rounded once.  A state that becomes
  * infinite or NaN stays so (either) along its paths and touches no other path.
  * C a multiple of 8 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
  * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at

@@ -237,7 +237,7 @@ def test_guards_around_every_buffer():
         return raw[4096:4096 + b].view(dtype).view(*shape)
 
     ws = guarded((tam.tree_scan_workspace(plan, C),), torch.uint8)
-    y, st = guarded((N, C), torch.bfloat16), guarded((n + plan.n_tiles, C), torch.float32)
+    y, st = guarded((N, C), torch.bfloat16), guarded((tam.tree_scan_rows(plan), C), torch.float32)
     dg, dx, di = guarded((N, C), torch.bfloat16), guarded((N, C), torch.bfloat16), guarded((n, C), torch.float32)
     tam.tree_scan_fwd(plan, tree, gate, x, init=init, workspace=ws, y=y, states=st)
     tam.tree_scan_bwd(plan, tree, gate, x, st, dy, init=init, d_final=dfin, workspace=ws, dgate=dg, dx=dx, d_init=di)

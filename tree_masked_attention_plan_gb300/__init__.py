@@ -9,7 +9,8 @@ functions carry the C entry points' names (``include/tree_attn.h``):
   tree_apply_weights, tree_attn_fwd, tree_attn_bwd_workspace, tree_attn_bwd,
   tree_attn_fwd_gateway, tree_attn_bwd_gateway, tree_relay_add, tree_gather_rows, tree_conv1d_fwd,
   tree_conv1d_bwd_workspace, tree_conv1d_bwd, tree_route_states, tree_route_states_bwd, tree_ce_workspace,
-  tree_ce_fwd_bwd, tree_rope_axes_fwd, tree_rope_axes_bwd, tree_scan_workspace, tree_scan_fwd, tree_scan_bwd,
+  tree_ce_fwd_bwd, tree_rope_axes_fwd, tree_rope_axes_bwd, tree_scan_rows, tree_scan_workspace, tree_scan_fwd,
+  tree_scan_bwd,
   tree_grad_norm, tree_grad_clip, tree_selftest_timeout, tree_set_wait_limit_ns (and diag_gemm -> tree_diag_gemm)
 
 Semantics follow "Tree Training 技术详解" (tingdeliu.github.io): DFS packing (section 3.2),
@@ -119,6 +120,7 @@ def _lib():
                                       _vp]),
         "tree_rope_axes_bwd": (_i32, [P(PlanT), _vp, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _f32,
                                       _vp]),
+        "tree_scan_rows": (_i64, [P(PlanT)]),
         "tree_scan_workspace": (ctypes.c_size_t, [P(PlanT), _i32]),
         "tree_scan_fwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
         "tree_scan_bwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
@@ -668,6 +670,11 @@ def tree_scan_workspace(plan: TreePlan, C) -> int:
     return int(_lib().tree_scan_workspace(plan.ref(), int(C)))
 
 
+def tree_scan_rows(plan: TreePlan) -> int:
+    """Rows of tree_scan_fwd's states: the nodes', then one for every 64 tokens."""
+    return int(_lib().tree_scan_rows(plan.ref()))
+
+
 def _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status):
     parent, node_len = tree
     if x.dim() != 2 or x.dtype not in _DTYPES:
@@ -697,9 +704,9 @@ def tree_scan_fwd(plan: TreePlan, tree, gate, x, init=None, gate_kind="sigmoid",
     """Gated linear recurrence along root paths: h_t = a_t h_prev(t) + b_t with a = sigmoid(gate), b = (1 - a) x
     (gate_kind "sigmoid") or a = exp(min(gate, 0)), b = x ("log").  gate, x [N, C] bf16 or fp32; init
     [n_nodes, C] fp32: the states that nodes without a token-holding ancestor start from.  Returns (y [N, C],
-    states [n_nodes + n_tiles, C] fp32): states[v] is node v's final state, the rest is for tree_scan_bwd."""
+    states [tree_scan_rows(plan), C] fp32): states[v] is node v's final state, the rest is for tree_scan_bwd."""
     C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
-    rows = n + plan.n_tiles
+    rows = tree_scan_rows(plan)
     if y is not None:
         _need_on(dev, y, x.shape, x.dtype, "y")
     if states is not None:
@@ -724,7 +731,7 @@ def tree_scan_bwd(plan: TreePlan, tree, gate, x, states, dy, init=None, d_final=
     d_init to write was given, else None."""
     C, dev, n, need = _scan_args(plan, tree, gate, x, init, gate_kind, workspace, status)
     _need_on(dev, dy, x.shape, x.dtype, "dy")
-    _need_on(dev, states, (n + plan.n_tiles, C), torch.float32, "states")
+    _need_on(dev, states, (tree_scan_rows(plan), C), torch.float32, "states")
     for t, what in ((dgate, "dgate"), (dx, "dx")):
         if t is not None:
             _need_on(dev, t, x.shape, x.dtype, what)
@@ -806,5 +813,5 @@ def tree_grad_clip(grads, max_norm, norm=None, stream=None):
     return _grad_call("tree_grad_clip", grads, norm, stream, max_norm)
 
 
-__all__ += ["tree_rope_axes_fwd", "tree_rope_axes_bwd", "tree_axis_positions", "tree_scan_workspace",
+__all__ += ["tree_rope_axes_fwd", "tree_rope_axes_bwd", "tree_axis_positions", "tree_scan_rows", "tree_scan_workspace",
             "tree_scan_fwd", "tree_scan_bwd", "GradList", "tree_grad_list", "tree_grad_norm", "tree_grad_clip"]

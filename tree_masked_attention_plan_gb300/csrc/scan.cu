@@ -10,7 +10,7 @@
 // final state of a node that lies before it.
 //
 // HBM-bound: the forward reads g and x and writes y once, the backward reads g, x, dy and writes
-// dg, dx once.  A unit of work is a tile of 128 tokens by 128 bytes of channels.  A step of the
+// dg, dx once.  A unit of work is a tile of 64 tokens by 128 bytes of channels.  A step of the
 // recurrence is the map h -> a h + b, and maps compose, so a tile needs its neighbours for one
 // value per channel only: it adds its own 128 steps up to one map, publishes that, takes the state
 // before it from the maps of the tiles before it, and then knows every h.  Tiles are handed out
@@ -33,15 +33,16 @@ int make_tmap_bf16_2d(CUtensorMap* m, const void* base, int inner, int rows, int
 
 namespace {
 
-constexpr int kScanWarps = 8;               // warps that share a tile: 16 tokens each
-constexpr int kFwdGroups = 2, kBwdGroups = 1;      // groups of mapping warps, which take tiles in turn
-constexpr int kEnds = 2;                            // tiles past the last that the loading warp announces as ends
-constexpr int kJoiners = 2;                         // joining warps, which take tiles in turn
-// a block: the mapping warps, the walking warps, one that loads, one that publishes, the joining ones
-constexpr int scan_threads(int groups) { return 32 * ((groups + 1) * kScanWarps + 2 + kJoiners); }
-constexpr int kWarpTokens = TILE / kScanWarps;
+constexpr int kTile = TREE_SCAN_TILE;       // tokens of a tile
+constexpr int kScanWarps = 8;               // warps that share a tile: 8 tokens each
+constexpr int kFwdSlots = kTile == 64 ? 6 : 3, kBwdSlots = kTile == 64 ? 5 : 3, kPlanes = 4;     // 160 to 192 KB: a block an SM
+// a block: mapping warps (eight times kFwdMaps, on one tile), groups of eight walking warps, one warp that loads, one
+// that publishes, some that join; groups and joining warps take tiles in turn
+constexpr int kFwdMaps = 2, kFwdWalks = 1, kFwdJoins = 3, kBwdMaps = 1, kBwdWalks = 1, kBwdJoins = 2;
+constexpr int scan_threads(int maps, int walks, int joins) { return 32 * ((maps + walks) * kScanWarps + 2 + joins); }
+constexpr int kWarpTokens = kTile / kScanWarps;
 constexpr int kRow = 128;                   // bytes of a tile's row: 64 bf16 or 32 fp32 channels, a word a lane
-constexpr int kPlane = TILE * kRow;         // one tensor's rows of a tile
+constexpr int kPlane = kTile * kRow;         // one tensor's rows of a tile
 constexpr int kScanGroup = 8;               // at most this many maps are joined to a state
 
 constexpr int kLinkChain = -1;             // the token before on the path is the one before in packed order
@@ -104,13 +105,13 @@ DEVI int link_of(int j, const ScanTree& t) {
 // Blocks (tile, share of the channels): links and info, the tile's flags cleared, its map and the state
 // behind it marked empty; and the rows that no tile writes are zeroed: those of nodes without tokens, and
 // with `inner` of nodes that do not start from nothing.
-__global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, int slabs, int C, int inner,
+__global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, int slabs, int C, int inner,
                                                        float* rows, float* between) {
   __shared__ int bits;
-  const int k = blockIdx.x, j = k * TILE + threadIdx.x;
+  const int k = blockIdx.x, j = k * kTile + threadIdx.x;
   {
     const uint4 e = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
-    const int first = blockIdx.y * TILE + threadIdx.x, step = gridDim.y * TILE;
+    const int first = blockIdx.y * kTile + threadIdx.x, step = gridDim.y * kTile;
     uint4* m = reinterpret_cast<uint4*>(w.maps + (size_t)k * C * 2);
     uint4* b = reinterpret_cast<uint4*>(between + (size_t)k * C);
     for (int i = first; i < C / 2; i += step) m[i] = e;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, i
   if (rows)
     for (int v = k; v < t.n_nodes; v += gridDim.x) {
       if (t.node_len[v] > 0 && !(inner && scan_token_ancestor(v, t) >= 0)) continue;
-      for (int c = blockIdx.y * TILE + threadIdx.x; c < C; c += gridDim.y * TILE) rows[(size_t)v * C + c] = 0.f;
+      for (int c = blockIdx.y * kTile + threadIdx.x; c < C; c += gridDim.y * kTile) rows[(size_t)v * C + c] = 0.f;
     }
   if (blockIdx.y) return;
   if (threadIdx.x == 0) bits = 0;
@@ -133,11 +134,11 @@ __global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, i
     if (link != kLinkChain) mine |= kInfoBreak;
     else if (threadIdx.x == 0) mine |= kInfoIn;
     if (link >= 0) {
-      if ((t.tok_start[link] + t.node_len[link] - 1) / TILE == k) mine |= kInfoSerial;
+      if ((t.tok_start[link] + t.node_len[link] - 1) / kTile == k) mine |= kInfoSerial;
       const int next = t.sub_end[v];
       if (next < t.sub_end[link]) {
         sib = t.tok_node[next];
-        if (next / TILE == k) mine |= kInfoSerialBack;
+        if (next / kTile == k) mine |= kInfoSerialBack;
       }
     }
     if (j == t.tok_start[v] + t.node_len[v] - 1) {
@@ -148,11 +149,11 @@ __global__ void __launch_bounds__(TILE) k_scan_prepare(ScanTree t, ScanWork w, i
         if (next < t.sub_end[v]) {
           kid = t.tok_node[next];
           mine |= kInfoSource;
-          if (next / TILE == k) mine |= kInfoSerialBack;
+          if (next / kTile == k) mine |= kInfoSerialBack;
         }
       }
     }
-    if (threadIdx.x == TILE - 1 && j + 1 < t.N && link_of(j + 1, t) == kLinkChain) mine |= kInfoOut;
+    if (threadIdx.x == kTile - 1 && j + 1 < t.N && link_of(j + 1, t) == kLinkChain) mine |= kInfoOut;
     w.link[j] = link;
     w.end[j] = end;
     w.kid[j] = kid;
@@ -271,6 +272,29 @@ DEVI Vec<CH> gate_of(Vec<CH> g) {
     }
   }
   return p;
+}
+
+// The forward's form of a token: decay a and input b.  Sigmoid: a = 1 / (1 + e) and 1 - a = e / (1 + e) with
+// e = e^-g, each with the relative accuracy of its own size; g is held above -87, where e is still finite and a
+// already below 2e-38.
+template <int KIND, int CH>
+DEVI void token_of(Vec<CH> g, Vec<CH> x, Vec<CH>& a, Vec<CH>& b) {
+  if (KIND == TREE_GATE_SIGMOID) {
+    Vec<CH> n, e;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) n.v[c] = max_nan(g.v[c], -87.f);
+    n = n * vec<CH>(-1.4426950408889634f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) e.v[c] = ex2_approx(n.v[c]);
+    const Vec<CH> d = e + vec<CH>(1.f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) a.v[c] = rcp_approx(d.v[c]);
+    b = (e * a) * x;
+  } else {
+    const Vec<CH> p = gate_of<TREE_GATE_LOG>(g);
+    a = p + pick(p, vec<CH>(1.f), vec<CH>(0.f));
+    b = x;
+  }
 }
 
 // A lane's word of a row: two bf16 channels or one fp32 channel.
@@ -427,47 +451,49 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
 }
 
 // A block works on up to SLOTS tiles at a time, in the order in which it drew them:
-//   loading warp      draws a tile, starts its copies                                       -> full, told
-//   mapping warps     the map of every token (backward: its p) and of every 16 tokens        -> mapped
-//   publishing warp   joins the 16-token maps to the tile's, hands that to the other blocks  -> known
+//   loading warp      draws a tile, starts its copies                                       -> drawn, full
+//   joining warp      looks up what the tile holds                                          -> told
+//   mapping warps     the map of every token (backward: its p) and of every warp's tokens    -> mapped
+//   publishing warp   joins the warps' maps to the tile's, hands that to the other blocks    -> known
 //   joining warp      finds the state before the tile, hands on the one behind it            -> ready
 //   walking warps     wait for that state, write the results                                 -> empty
 // So a tile whose state is late holds up nothing that another tile waits for: its map is out, and so are
-// those of the tiles that the block drew after it.  Forward, 32768 tokens x 8192 channels bf16: 0.86 ms
-// where one set of warps took a tile from its copies to its results, waiting in between.
-template <int SLOTS>
+// those of the tiles that the block drew after it.
+template <int SLOTS, int MAPS>
 struct ScanShared {
-  uint64_t full[SLOTS], told[SLOTS], mapped[SLOTS], known[SLOTS], ready[SLOTS], empty[SLOTS];
-  // Among the walking warps: done, a tile's rows are written (one for each slot: only one warp waits there, and
-  // one that is a tile ahead must not be counted for this one); own, their own maps are there (all wait); turn,
-  // the warp before is through.
-  uint64_t done[SLOTS], own, turn[kScanWarps];
-  int tile[SLOTS], slab[SLOTS], info[SLOTS], dist[SLOTS];
+  uint64_t drawn[SLOTS], full[SLOTS], told[SLOTS], mapped[SLOTS], known[SLOTS], ready[SLOTS], empty[SLOTS];
+  int tile[SLOTS], slab[SLOTS], info[SLOTS];
   int abort_flag;
   int reset[SLOTS][kScanWarps];
-  alignas(16) float A[SLOTS][kScanWarps][64];      // per warp and channel: the map of its 16 tokens
-  alignas(16) float B[SLOTS][kScanWarps][64];
+  // Per warp and channel the map of its tokens; in a tile without breaks the publishing warp puts that of all
+  // tokens before the warp there (backward: in B the state before it, in A and R the gradient's map behind it).
+  alignas(16) float A[SLOTS][kScanWarps * MAPS][64];
+  alignas(16) float B[SLOTS][kScanWarps * MAPS][64];
   alignas(16) float all[SLOTS][2][64];             // the tile's map
   alignas(16) float in[SLOTS][64];                 // the state before (the gradient behind) the tile
-  alignas(16) float carry[kScanWarps][64];         // the same for a warp, in tiles that go warp by warp
 };
-template <int SLOTS>
+using FwdShared = ScanShared<kFwdSlots, kFwdMaps>;
+using BwdShared = ScanShared<kBwdSlots, kBwdMaps>;
+// A group of walking warps among themselves.
+struct ScanWalk {
+  uint64_t own, turn[kScanWarps];                  // their own maps are there (all wait); the warp before is through
+  alignas(16) float carry[kScanWarps][64];         // the state before (gradient behind) a warp, where they go one by one
+};
 struct ScanBack {
-  alignas(16) float R[SLOTS][kScanWarps][64];      // the gradient's map is u -> A u + R
-  alignas(16) float before[kScanWarps][4][64];     // h before every fourth token, where it cannot stay in registers
+  alignas(16) float R[kBwdSlots][kScanWarps][64];      // the gradient's map is u -> A u + R
+  alignas(16) float before[kScanWarps][kWarpTokens / 4][64];     // h before every fourth token, where it cannot stay in registers
 };
 
-// Forward: the states behind nodes that end in the tile at hand, one for every four tokens (the last that came).
+// Forward: the states behind nodes that end in the tile at hand, one for every kKeep tokens (the last that came).
+constexpr int kKeep = 8;
 struct ScanEnds {
-  int token[TILE / 4];                             // which token's
-  alignas(16) float state[TILE / 4][64];
+  int token[kTile / kKeep];                         // which token's
+  alignas(16) float state[kTile / kKeep][64];
 };
 
-constexpr int kSlots = 3, kPlanes = 4;             // 192 KB: a block an SM
 
 template <typename T>
 struct ScanFwd {
-  const T *gate, *x;
   const float* init;
   T* y;
   float* states;
@@ -490,28 +516,28 @@ struct ScanBwd {
   uint64_t limit_ns;
 };
 
-// The loading warp: draws tiles from the counter, starts their copies, and finds how many maps lie
-// between the tile and the state it starts from.  FWD: that is the state behind the nearest tile before
-// it that is no plain map or ends a group of kScanGroup; backward the same from the other side.
-// Groups bound the maps that a tile joins; within one, no tile waits for a state to be handed on.
-template <bool FWD, int TENSORS>
-DEVI void scan_load(ScanShared<kSlots>& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
-                    int tiles, int slabs, int slab_ch, bool joins, const WaitCtl& wc) {
+// The loading warp: draws tiles from the counter and starts their copies.
+template <bool FWD, int SLOTS, int MAPS, int TENSORS>
+DEVI void scan_load(ScanShared<SLOTS, MAPS>& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
+                    int tiles, int slabs, int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   auto draw = [&] { return atomicAdd(reinterpret_cast<unsigned long long*>(w.ctl), 1ull); };
   unsigned long long next = lane == 0 ? draw() : 0;
   int i = 0, ends = 0;
   for (;; ++i) {
-    const int s = i % kSlots;
-    if (i >= kSlots && !wait_phase(&sh.empty[s], ((i / kSlots) - 1) & 1, wc)) break;
+    const int s = i % SLOTS;
+    if (i >= SLOTS && !wait_phase(&sh.empty[s], ((i / SLOTS) - 1) & 1, wc)) break;
     const unsigned long long ticket = __shfl_sync(0xffffffffu, next, 0);
-    const unsigned long long turn = ticket / (unsigned)slabs;    // tile by tile, its slabs side by side
+    // tile by tile, its slabs side by side
+    const unsigned long long turn = ticket >> 32 ? ticket / (unsigned)slabs : (uint32_t)ticket / (uint32_t)slabs;
     if (turn >= (unsigned)tiles) {                   // the end, for all that take tiles in turn
       if (lane == 0) {
         sh.tile[s] = -1;
+        mbar_arrive(&sh.drawn[s]);
+        mbar_arrive(&sh.told[s]);
         mbar_arrive(&sh.full[s]);
       }
-      if (++ends == kEnds) break;
+      if (++ends == SLOTS) break;
       continue;
     }
     const int slab = static_cast<int>(ticket - turn * (unsigned)slabs);
@@ -519,35 +545,25 @@ DEVI void scan_load(ScanShared<kSlots>& sh, uint8_t* slots, const CUtensorMap* c
     if (lane == 0) {
       sh.tile[s] = k;
       sh.slab[s] = slab;
+      mbar_arrive(&sh.drawn[s]);
       mbar_expect_tx(&sh.full[s], TENSORS * kPlane);
 #pragma unroll
       for (int a = 0; a < TENSORS; ++a)
-        tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * TILE);
+        tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * kTile);
     }
     // The first tiles are drawn one at a time, so that neighbours go to different blocks; later ones ahead.
-    if (i + 1 < kSlots && !wait_phase(&sh.full[s], 0, wc)) {
+    if (i + 1 < SLOTS && !wait_phase(&sh.full[s], 0, wc)) {
       ++i;
       break;
     }
     if (lane == 0) next = draw();
-    const int j = FWD ? k - lane : k + lane;
-    int info = (lane <= kScanGroup && j >= 0 && j < tiles) ? w.info[j] : kInfoBreak;
-    // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
-    const bool mapped = !(info & kInfoBreak) && (FWD || !(info & kInfoSource || (joins && (info & kInfoEnd))));
-    const bool map = mapped && (FWD ? (j + 1) % kScanGroup != 0 : (info & kInfoOut) && j % kScanGroup != 0);
-    const uint32_t run = __ballot_sync(0xffffffffu, map);
-    if (lane == 0) {
-      sh.info[s] = info | (mapped ? kInfoMapped : 0) | (map ? kInfoMap : 0);
-      sh.dist[s] = __ffs(~(run >> 1)) - 1;
-      mbar_arrive(&sh.told[s]);
-    }
   }
   // every copy has landed before the block's shared memory goes, also where other warps gave up
   // (slots that hold an end had their copies used before)
   if (lane == 0)
-    for (int q = max(0, i - kSlots); q < i; ++q) {
+    for (int q = max(0, i - SLOTS); q < i; ++q) {
       const uint64_t t0 = global_timer_ns();
-      while (sh.tile[q % kSlots] >= 0 && !mbar_try_wait(&sh.full[q % kSlots], (q / kSlots) & 1) &&
+      while (sh.tile[q % SLOTS] >= 0 && !mbar_try_wait(&sh.full[q % SLOTS], (q / SLOTS) & 1) &&
              global_timer_ns() - t0 < wc.limit_ns) {
       }
     }
@@ -555,39 +571,36 @@ DEVI void scan_load(ScanShared<kSlots>& sh, uint8_t* slots, const CUtensorMap* c
 
 // The next tile of a warp that is not the loading one; false at the end, or where a wait gave up.
 struct Tile {
-  int k, slab, info, dist, s;
+  int k, slab, info, s;
   uint32_t parity;
 };
-DEVI bool next_tile(ScanShared<kSlots>& sh, int i, Tile& t, const WaitCtl& wc) {
-  t.s = i % kSlots;
-  t.parity = (i / kSlots) & 1;
-  if (!wait_phase(&sh.full[t.s], t.parity, wc)) return false;
+// `bar`: what of the tile is waited for; a tile number of -1 there is the end
+template <int SLOTS, int MAPS>
+DEVI bool next_tile(ScanShared<SLOTS, MAPS>& sh, uint64_t (&bar)[SLOTS], int i, Tile& t, const WaitCtl& wc) {
+  t.s = i % SLOTS;
+  t.parity = (i / SLOTS) & 1;
+  if (!wait_phase(&bar[t.s], t.parity, wc)) return false;
   t.k = sh.tile[t.s];
   t.slab = sh.slab[t.s];
+  t.info = sh.info[t.s];                             // (valid from `told` on)
   return t.k >= 0;
-}
-DEVI bool tile_info(ScanShared<kSlots>& sh, Tile& t, const WaitCtl& wc) {
-  if (!wait_phase(&sh.told[t.s], t.parity, wc)) return false;
-  t.info = sh.info[t.s];
-  t.dist = sh.dist[t.s];
-  return true;
 }
 DEVI void warp_arrive(uint64_t* bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
-// A lane's words of a warp's 16 rows of a slot.  Planes 0, 1 (and backward 2) hold the tensors' rows.
-// Forward, a token's map takes their place: A and B of the lane's first channel in planes 0 and 1, those of
-// the second side by side in planes 2 and 3.  Backward, p does: first channel in plane 0, second in plane 3.
+// A lane's words of a warp's 16 rows of a slot.  Planes 0, 1 (and backward 2) hold the tensors' rows.  Forward,
+// a and b take their place: those of the lane's first channel in planes 0 and 1, of the second side by side in
+// planes 2 and 3.  Backward, p does: first channel in plane 0, second in plane 3.
 template <typename T>
 struct Rows {
   uint8_t *base, *pair;
   static constexpr int CH = Lane<T>::CH;
-  DEVI Rows(uint8_t* slots, int s, int warp) {
-    const int lane = threadIdx.x & 31;
-    base = slots + (size_t)s * kPlanes * kPlane + warp * kWarpTokens * kRow + lane * 4;
-    pair = slots + ((size_t)s * kPlanes + 2) * kPlane + warp * kWarpTokens * 2 * kRow + lane * 8;
+  DEVI Rows(uint8_t* slots, int s, int warp, int first = 0) {
+    const int lane = threadIdx.x & 31, row = warp * kWarpTokens + first;
+    base = slots + (size_t)s * kPlanes * kPlane + row * kRow + lane * 4;
+    pair = slots + ((size_t)s * kPlanes + 2) * kPlane + row * 2 * kRow + lane * 8;
   }
   DEVI float& word(int plane, int i) const { return *reinterpret_cast<float*>(base + plane * kPlane + i * kRow); }
   DEVI Vec<CH> get(int plane, int i) const { return Lane<T>::unpack(__float_as_uint(word(plane, i))); }
@@ -601,27 +614,21 @@ struct Rows {
     word(0, i) = v.v[0];
     if constexpr (CH == 2) word(3, i) = v.v[1];
   }
-  DEVI void set_map(int i, Vec<CH> A, Vec<CH> B) const {
-    word(0, i) = A.v[0];
-    word(1, i) = B.v[0];
-    if constexpr (CH == 2) *reinterpret_cast<float2*>(pair + i * 2 * kRow) = make_float2(A.v[1], B.v[1]);
+  DEVI void set_token(int i, Vec<CH> a, Vec<CH> b) const {
+    word(0, i) = a.v[0];
+    word(1, i) = b.v[0];
+    if constexpr (CH == 2) *reinterpret_cast<float2*>(pair + i * 2 * kRow) = make_float2(a.v[1], b.v[1]);
   }
-  DEVI Vec<CH> constant(int i) const {               // B alone
-    Vec<CH> B;
-    B.v[0] = word(1, i);
-    if constexpr (CH == 2) B.v[1] = reinterpret_cast<const float2*>(pair + i * 2 * kRow)->y;
-    return B;
-  }
-  DEVI Vec<CH> mapped(int i, Vec<CH> h) const {      // the token's map of the state before the warp
-    Vec<CH> A, B;
-    A.v[0] = word(0, i);
-    B.v[0] = word(1, i);
+  DEVI Vec<CH> step(int i, Vec<CH> h) const {        // a h + b
+    Vec<CH> a, b;
+    a.v[0] = word(0, i);
+    b.v[0] = word(1, i);
     if constexpr (CH == 2) {
       const float2 m = *reinterpret_cast<const float2*>(pair + i * 2 * kRow);
-      A.v[1] = m.x;
-      B.v[1] = m.y;
+      a.v[1] = m.x;
+      b.v[1] = m.y;
     }
-    return vfma(A, h, B);
+    return vfma(a, h, b);
   }
 };
 
@@ -668,20 +675,22 @@ struct Joiner {
 };
 
 // The publishing warp.  It waits for no other block, so that a tile's map is out as soon as it can be.
-template <bool FWD, int CH>
-DEVI void scan_publish(ScanShared<kSlots>& sh, const float (*add)[kScanWarps][64], const ScanWork& w, int C,
-                       int slab_ch, const WaitCtl& wc) {
+template <int CH>
+DEVI void fwd_publish(FwdShared& sh, const ScanWork& w, int C, int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
-  for (int i = 0; next_tile(sh, i, t, wc) && tile_info(sh, t, wc); ++i) {
+  for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
     if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
     if (t.info & kInfoMapped) {
       Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
-#pragma unroll
-      for (int n = 0; n < kScanWarps; ++n) {
-        const int q = FWD ? n : kScanWarps - 1 - n;
-        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]);
-        B = vfma(qa, B, sh_ld<CH>(add[t.s][q]));
+#pragma unroll 8
+      for (int q = 0; q < kScanWarps * kFwdMaps; ++q) {
+        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]), qb = sh_ld<CH>(sh.B[t.s][q]);
+        if (q % kFwdMaps == 0) {
+          sh_st(sh.A[t.s][q], A);
+          sh_st(sh.B[t.s][q], B);
+        }
+        B = vfma(qa, B, qb);
         A = A * qa;
       }
       const int ch = t.slab * slab_ch + lane * CH;
@@ -693,166 +702,199 @@ DEVI void scan_publish(ScanShared<kSlots>& sh, const float (*add)[kScanWarps][64
   }
 }
 
-// A joining warp.  rows: the states between tiles (backward: the gradients).
-template <bool FWD, int CH>
-DEVI void scan_join(ScanShared<kSlots>& sh, const ScanWork& w, int C, float* rows, int slab_ch, int joiner,
-                    const WaitCtl& wc) {
+// after: the states between tiles, which the forward left
+template <int CH>
+DEVI void bwd_publish(BwdShared& sh, ScanBack& back, const ScanWork& w, const float* after, int C,
+                      int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
-  for (int i = joiner; next_tile(sh, i, t, wc) && tile_info(sh, t, wc); i += kJoiners) {
+  for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
     const int ch = t.slab * slab_ch + lane * CH;
-    const bool on = ch < C, need = t.info & (FWD ? kInfoIn : kInfoOut);
-    const int b = FWD ? t.k - 1 - t.dist : t.k + 1 + t.dist;
-    const Joiner<CH> j{w, C, ch, b, FWD ? 1 : -1, t.dist, rows + (size_t)(need ? b : 0) * C + ch, on};
+    Vec<CH> h = ld_state_if(after + ((size_t)t.k * C - C) + ch, ch < C && (t.info & kInfoIn), Vec<CH>());
+    if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+    if (t.info & kInfoMapped) {
+#pragma unroll
+      for (int q = 0; q < kScanWarps; ++q) {
+        const Vec<CH> qb = sh_ld<CH>(sh.B[t.s][q]);
+        sh_st(sh.B[t.s][q], h);
+        h = vfma(sh_ld<CH>(sh.A[t.s][q]), h, qb);
+      }
+      Vec<CH> A = vec<CH>(1.f), R = vec<CH>(0.f);
+#pragma unroll
+      for (int q = kScanWarps - 1; q >= 0; --q) {
+        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]), qr = sh_ld<CH>(back.R[t.s][q]);
+        sh_st(sh.A[t.s][q], A);
+        sh_st(back.R[t.s][q], R);
+        R = vfma(qa, R, qr);
+        A = A * qa;
+      }
+      if ((t.info & kInfoMap) && ch < C) hand_map(w.maps + ((size_t)t.k * C + ch) * 2, A, R);
+      sh_st(sh.all[t.s][0], A);
+      sh_st(sh.all[t.s][1], R);
+    }
+    warp_arrive(&sh.known[t.s]);
+  }
+}
+
+// A joining warp.  It finds how many maps lie between the tile and the state it starts from.  FWD: that is the
+// state behind the nearest tile before it that is no plain map or ends a group of kScanGroup; backward the same
+// from the other side.  Groups bound the maps that a tile joins; within one, no tile waits for a state to be
+// handed on.  rows: the states between tiles (backward: the gradients).
+template <bool FWD, int CH, int JOINS, int SLOTS, int MAPS>
+DEVI void scan_join(ScanShared<SLOTS, MAPS>& sh, const ScanWork& w, int C, int tiles, float* rows, int slab_ch, bool joins,
+                    int joiner, const WaitCtl& wc) {
+  const int lane = threadIdx.x & 31;
+  Tile t;
+  for (int i = joiner; next_tile(sh, sh.drawn, i, t, wc); i += JOINS) {
+    const int n = FWD ? t.k - lane : t.k + lane;
+    int info = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
+    // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
+    const bool mapped = !(info & kInfoBreak) && (FWD || !(info & kInfoSource || (joins && (info & kInfoEnd))));
+    const bool map = mapped && (FWD ? (n + 1) % kScanGroup != 0 : (info & kInfoOut) && n % kScanGroup != 0);
+    const uint32_t run = __ballot_sync(0xffffffffu, map);
+    info = __shfl_sync(0xffffffffu, info | (mapped ? kInfoMapped : 0) | (map ? kInfoMap : 0), 0);
+    if (lane == 0) sh.info[t.s] = info;
+    warp_arrive(&sh.told[t.s]);
+    const int ch = t.slab * slab_ch + lane * CH, dist = __ffs(~(run >> 1)) - 1;
+    const bool on = ch < C, need = info & (FWD ? kInfoIn : kInfoOut);
+    const int b = FWD ? t.k - 1 - dist : t.k + 1 + dist;
+    const Joiner<CH> j{w, C, ch, b, FWD ? 1 : -1, dist, rows + (size_t)(need ? b : 0) * C + ch, on};
     Vec<CH> v = vec<CH>(0.f);
     if (need && !j.join(v, wc)) {
       if (lane == 0) sh.abort_flag = 1;
       return;
     }
+    if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
+    if ((info & kInfoMapped) && on)
+      hand_state(rows + (size_t)t.k * C + ch, vfma(sh_ld<CH>(sh.all[t.s][0]), v, sh_ld<CH>(sh.all[t.s][1])));
     sh_st<CH>(sh.in[t.s], v);
     warp_arrive(&sh.ready[t.s]);
-    if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
-    if ((t.info & kInfoMapped) && on)
-      hand_state(rows + (size_t)t.k * C + ch, vfma(sh_ld<CH>(sh.all[t.s][0]), v, sh_ld<CH>(sh.all[t.s][1])));
     warp_arrive(&sh.empty[t.s]);
   }
 }
 
-// The mapping warps, forward: every token's map of the state before its warp.
-template <typename T, int KIND, int GROUPS>
-DEVI void fwd_map(ScanShared<kSlots>& sh, uint8_t* slots, int group, int warp, const WaitCtl& wc) {
+// The mapping warps, forward, all on one tile: a and b of every token, and the map of kMapTokens of them.
+constexpr int kMapTokens = kWarpTokens / kFwdMaps;
+template <typename T, int KIND>
+DEVI void fwd_map(FwdShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH;
   Tile t;
-  for (int i = group; next_tile(sh, i, t, wc); i += GROUPS) {
-    const Rows<T> rows(slots, t.s, warp);
+  for (int i = 0; next_tile(sh, sh.full, i, t, wc); ++i) {
+    const Rows<T> rows(slots, t.s, warp / kFwdMaps, warp % kFwdMaps * kMapTokens);
     Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
 #pragma unroll 4
-    for (int q = 0; q < kWarpTokens; ++q) {
-      const Vec<CH> p = gate_of<KIND>(rows.get(0, q));
-      B = advance<KIND>(p, rows.get(1, q), B);
-      A = decayed(p, A);
-      rows.set_map(q, A, B);
+    for (int q = 0; q < kMapTokens; ++q) {
+      Vec<CH> a, b;
+      token_of<KIND>(rows.get(0, q), rows.get(1, q), a, b);
+      rows.set_token(q, a, b);
+      B = vfma(a, B, b);
+      A = A * a;
     }
     sh_st(sh.A[t.s][warp], A);
     sh_st(sh.B[t.s][warp], B);
-    fence_proxy_async_smem();                          // the maps lie where the next copies go
+    fence_proxy_async_smem();                          // a and b lie where the next copies go
     warp_arrive(&sh.mapped[t.s]);
   }
 }
 
-// Forward, a warp whose 16 tokens hold breaks: the mapping warps' maps do not reach across one.  (Its loops are
-// rolled: this is rare, and straight-line code for it would be fetched anew each time.)
-template <typename T, int KIND>
-struct FwdBreaks {
+// Forward, the runs of a warp's 8 tokens between breaks and what is to be kept of them.  Loops are rolled: this
+// is rare, and straight-line code for it would be fetched anew each time.
+template <typename T>
+struct FwdRuns {
   static constexpr int CH = Lane<T>::CH;
   const ScanFwd<T>& a;
   const Rows<T>& rows;
   ScanEnds& kept;
   int k, t0, ch;
   bool on;
-  int from, end;                           // per lane q < 16: link of token t0 + q, its node if it is the node's last
+  int from, end;                           // per lane q < 8: link of token t0 + q, its node if it is the node's last
   uint32_t breaks, ends, reset;            // a bit a token; reset: breaks that start from outside the tile
-  // New maps for the 16 tokens, from g and x in global memory, four at a time with their loads in flight
-  // together.  Behind a break they start anew: from outside the tile with the state itself, as a constant in B;
-  // from a node of this tile as maps of that node's state, which is not known yet.
-  DEVI Vec<CH> remap(Vec<CH>& A) const {
-    Vec<CH> B = vec<CH>(0.f);
-    A = vec<CH>(1.f);
+  DEVI uint32_t behind(int q) const { return q < 31 ? ~((2u << q) - 1u) : 0u; }
+  DEVI int run_end(int q) const {
+    const uint32_t m = breaks & behind(q);
+    return m ? __ffs(m) - 1 : kWarpTokens;
+  }
+  // the tokens from q0 to the next break, h the state before them; returns the state behind them
+  DEVI Vec<CH> run(Vec<CH> h, int q0) const {
+    const int q1 = run_end(q0);
 #pragma unroll 1
-    for (int g = 0; g < kWarpTokens; g += 4) {
+    for (int q = q0; q < q1; ++q) {
+      h = rows.step(q, h);
+      if (on && t0 + q < a.t.N) *reinterpret_cast<uint32_t*>(a.y + (size_t)(t0 + q) * a.C + ch) = Lane<T>::pack(h);
+      if ((ends >> q) & 1u) {              // a node's last token: its state, for the user and for breaks
+        const int e = __shfl_sync(0xffffffffu, end, q), tok = t0 + q - k * kTile, slot = tok / kKeep;
+        if (on) st_state(a.states + (size_t)e * a.C + ch, h);
+        sh_st(kept.state[slot], h);
+        if ((threadIdx.x & 31) == 0) kept.token[slot] = tok;
+        __syncwarp();
+      }
+    }
+    return h;
+  }
+  // All runs that start from outside the tile, which wait for nothing here: true if the last run is one of them,
+  // whose end is then the state behind the warp.
+  DEVI bool known_runs(Vec<CH>& last) const {
+#pragma unroll 1
+    for (uint32_t m = reset; m;) {
+      // the starts of four runs at a time: their loads are in flight together
       Vec<CH> s[4];
-      uint32_t gw[4], xw[4];
+      int q[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = __shfl_sync(0xffffffffu, from, g + q);
-        const bool start = (reset >> (g + q)) & 1u;
+      for (int r = 0; r < 4; ++r) {
+        q[r] = m ? __ffs(m) - 1 : -1;
+        m &= m - 1;
+        const int n = __shfl_sync(0xffffffffu, from, max(q[r], 0));
         const float* row = n >= 0 ? a.states + (size_t)n * a.C
-                                  : (a.init && start ? a.init + (size_t)a.t.tok_node[t0 + g + q] * a.C : nullptr);
-        s[q] = ld_state_if(row + ch, on && row && start, B);
-        const bool live = on && t0 + g + q < a.t.N;
-        const size_t at = (size_t)(t0 + g + q) * a.C + ch;
-        gw[q] = live ? *reinterpret_cast<const uint32_t*>(a.gate + at) : 0u;
-        xw[q] = live ? *reinterpret_cast<const uint32_t*>(a.x + at) : 0u;
+                                  : (a.init && q[r] >= 0 ? a.init + (size_t)a.t.tok_node[t0 + q[r]] * a.C : nullptr);
+        s[r] = ld_state_if(row + ch, on && row && q[r] >= 0, last);
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if ((breaks >> (g + q)) & 1u) {
-          A = vec<CH>(1.f);
-          B = ((reset >> (g + q)) & 1u) ? s[q] : vec<CH>(0.f);
-        }
-        const Vec<CH> p = gate_of<KIND>(Lane<T>::unpack(gw[q]));
-        B = advance<KIND>(p, Lane<T>::unpack(xw[q]), B);
-        A = decayed(p, A);
-        rows.set_map(g + q, A, B);
-      }
-    }
-    return B;
-  }
-  // The state that the run of tokens behind the break at q starts from, a node of this tile's.
-  DEVI Vec<CH> source(int q) const {
-    const int n = __shfl_sync(0xffffffffu, from, q);
-    const int tok = a.t.tok_start[n] + a.t.node_len[n] - 1 - k * TILE, slot = tok / 4;
-    if (kept.token[slot] == tok) return sh_ld<CH>(kept.state[slot]);
-    return ld_state_if(a.states + (size_t)n * a.C + ch, on, Vec<CH>());     // another end has taken its place
-  }
-  DEVI void keep(int q, Vec<CH> v) const {   // the state of the node that ends at q
-    const int e = __shfl_sync(0xffffffffu, end, q), tok = t0 + q - k * TILE, slot = tok / 4;
-    if (on) st_state(a.states + (size_t)e * a.C + ch, v);
-    sh_st(kept.state[slot], v);
-    if ((threadIdx.x & 31) == 0) kept.token[slot] = tok;
-    __syncwarp();
-  }
-  // Through the tokens at which something happens; h: the state before the warp.  Returns the state behind it.
-  DEVI Vec<CH> pass(Vec<CH> h, bool keeping) const {
-    bool set = false;                        // the run's states are in B already
-    for (uint32_t m = (breaks & ~reset) | reset | (keeping ? ends : 0u); m; m &= m - 1) {
-      const int q = __ffs(m) - 1;
-      if ((breaks >> q) & 1u) {
-        set = (reset >> q) & 1u;
-        if (!set) h = source(q);
-      }
-      if ((ends >> q) & 1u) {
-        const Vec<CH> v = set ? rows.constant(q) : rows.mapped(q, h);
-        if (keeping) keep(q, v);
-      }
-    }
-    return set ? rows.constant(kWarpTokens - 1) : rows.mapped(kWarpTokens - 1, h);
-  }
-  DEVI void write(Vec<CH> h) const {
-    bool set = false;
 #pragma unroll 1
-    for (int q = 0; q < kWarpTokens; ++q) {
-      if ((breaks >> q) & 1u) {
-        set = (reset >> q) & 1u;
-        if (!set) h = source(q);
+      for (int r = 0; r < 4; ++r) {
+        if (q[0] < 0) break;
+        last = run(s[0], q[0]);
+        s[0] = s[1]; s[1] = s[2]; s[2] = s[3];
+        q[0] = q[1]; q[1] = q[2]; q[2] = q[3]; q[3] = -1;
       }
-      const Vec<CH> v = set ? rows.constant(q) : rows.mapped(q, h);
-      if (on && t0 + q < a.t.N) *reinterpret_cast<uint32_t*>(a.y + (size_t)(t0 + q) * a.C + ch) = Lane<T>::pack(v);
     }
+    return reset && (breaks >> (31 - __clz(reset))) == 1u;
+  }
+  // The runs that wait: the one that comes into the warp, and those that start from nodes of this tile.  Returns
+  // the state behind the last of them.
+  DEVI Vec<CH> waiting_runs(Vec<CH> h) const {
+    if (!(breaks & 1u)) h = run(h, 0);
+#pragma unroll 1
+    for (uint32_t m = breaks & ~reset; m; m &= m - 1) {
+      const int q = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, from, q);
+      const int tok = a.t.tok_start[n] + a.t.node_len[n] - 1 - k * kTile, slot = tok / kKeep;
+      // kept, unless the end of another node within the same tokens has taken its place
+      h = kept.token[slot] == tok ? sh_ld<CH>(kept.state[slot]) : ld_state_if(a.states + (size_t)n * a.C + ch, on, h);
+      h = run(h, q);
+    }
+    return h;
   }
 };
 
 // The walking warps, forward.  Returns where a wait gave up or the tiles have ended.
-template <typename T, int KIND>
-DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, ScanEnds& kept, uint8_t* slots, int warp,
-                   const WaitCtl& wc) {
+template <typename T>
+DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& kept, uint8_t* slots,
+                   int group, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t n_own = 0, n_turn = 0;                      // uses of the walking warps' barriers so far
   Tile t;
-  for (int i = 0; next_tile(sh, i, t, wc) && tile_info(sh, t, wc); ++i) {
+  for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kFwdWalks) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;          // the lane's first channel
-    const int t0 = t.k * TILE + warp * kWarpTokens;
-    FwdBreaks<T, KIND> f{a, rows, kept, t.k, t0, ch, ch < a.C, kLinkChain, -1, 0u, 0u, 0u};
-    const bool serial = t.info & kInfoSerial;
-    if (t.info & (kInfoBreak | kInfoEnd)) {
+    const int t0 = t.k * kTile + warp * kWarpTokens;
+    FwdRuns<T> f{a, rows, kept, t.k, t0, ch, ch < a.C, kLinkChain, -1, 0u, 0u, 0u};
+    const bool serial = t.info & kInfoSerial, special = t.info & (kInfoBreak | kInfoEnd);
+    if (special) {
       bool ok = true, tile = false;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
         f.from = a.w.link[t0 + lane];
         f.end = a.w.end[t0 + lane];
         if (f.from >= 0) {
-          const int ts = (a.t.tok_start[f.from] + a.t.node_len[f.from] - 1) / TILE;
+          const int ts = (a.t.tok_start[f.from] + a.t.node_len[f.from] - 1) / kTile;
           tile = ts == t.k;
           if (!tile) ok = wait_rows(a.w.flags + (size_t)ts * a.slabs + t.slab, wc, a.w.ctl + 2);
         }
@@ -865,83 +907,86 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared<kSlots>& sh, ScanEnds& kept, 
       f.ends = __ballot_sync(0xffffffffu, f.end >= 0);
       f.reset = f.breaks & ~__ballot_sync(0xffffffffu, tile);
     }
-    if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+    Vec<CH> last = vec<CH>(0.f);                       // the state behind the warp
+    bool last_known = false;
     if (t.info & kInfoBreak) {
-      if (f.breaks) {
-        Vec<CH> A;
-        const Vec<CH> B = f.remap(A);
-        sh_st(sh.B[t.s][warp], B);                     // (a tile whose warps go one by one has no use for it)
+      if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+      if (serial) {                                    // no warp is a tile ahead, where its turn would overtake this one's
+        if (lane < kTile / kKeep / kScanWarps) kept.token[warp * (kTile / kKeep / kScanWarps) + lane] = -1;
+        warp_arrive(&g.own);
+        if (!wait_phase(&g.own, n_own & 1, wc)) return;
+        ++n_own;
       }
-      if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
-      if (serial && lane < TILE / 4 / kScanWarps) kept.token[warp * (TILE / 4 / kScanWarps) + lane] = -1;
-      // All maps are there; and no warp is a tile ahead, where its next turn would overtake this one's.
-      warp_arrive(&sh.own);
-      if (!wait_phase(&sh.own, n_own & 1, wc)) return;
-      ++n_own;
+      last_known = f.known_runs(last);
+      if (!serial) {                                   // every warp's map is there
+        if (f.breaks) sh_st(sh.B[t.s][warp * kFwdMaps], last);
+        if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
+        warp_arrive(&g.own);
+        if (!wait_phase(&g.own, n_own & 1, wc)) return;
+        ++n_own;
+      }
     }
     // The state before the warp: from the maps of the warps before it; where a break starts from a node that
     // ends in this very tile, from the warp before it, which has then kept its nodes' states.
-    Vec<CH> h;
-    if (!serial) {
-      Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
-      bool fixed = false;
+    auto past = [&](int q, Vec<CH> v) {                // the state behind warp q's tokens, by their maps
 #pragma unroll
-      for (int q = 0; q < kScanWarps - 1; ++q) {
-        if (q >= warp) break;
-        const bool r = (t.info & kInfoBreak) && sh.reset[t.s][q];
-        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]), qb = sh_ld<CH>(sh.B[t.s][q]);
-        B = r ? qb : vfma(qa, B, qb);
-        A = A * qa;
-        fixed |= r;
-      }
-      if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
-      h = fixed ? B : vfma(A, sh_ld<CH>(sh.in[t.s]), B);
+      for (int m = 0; m < kFwdMaps; ++m)
+        v = vfma(sh_ld<CH>(sh.A[t.s][q * kFwdMaps + m]), v, sh_ld<CH>(sh.B[t.s][q * kFwdMaps + m]));
+      return v;
+    };
+    if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
+    Vec<CH> h = sh_ld<CH>(sh.in[t.s]);
+    if (t.info & kInfoMapped) {
+      h = vfma(sh_ld<CH>(sh.A[t.s][warp * kFwdMaps]), h, sh_ld<CH>(sh.B[t.s][warp * kFwdMaps]));
+    } else if (!serial) {
+      for (int q = 0; q < warp; ++q) h = sh.reset[t.s][q] ? sh_ld<CH>(sh.B[t.s][q * kFwdMaps]) : past(q, h);
     } else {
-      if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
-      if (warp > 0 && !wait_phase(&sh.turn[warp], n_turn & 1, wc)) return;
+      if (warp > 0) {
+        if (!wait_phase(&g.turn[warp], n_turn & 1, wc)) return;
+        h = sh_ld<CH>(g.carry[warp - 1]);
+      }
       ++n_turn;
-      h = sh_ld<CH>(warp > 0 ? sh.carry[warp - 1] : sh.in[t.s]);
     }
-    // first what others wait for: nodes' states, and the state behind the warp
     int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
-    if (t.info & (kInfoBreak | kInfoEnd)) {
-      const Vec<CH> last = f.pass(h, true);
+    auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles behind
       if (serial && warp < kScanWarps - 1) {
-        sh_st(sh.carry[warp], last);
-        warp_arrive(&sh.turn[warp + 1]);
+        sh_st(g.carry[warp], v);
+        warp_arrive(&g.turn[warp + 1]);
       }
       if ((t.info & kInfoBreak) && warp == kScanWarps - 1) {
-        if (f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, last);
+        if (f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
         if (serial) publish(flag);
       }
-    }
-    if (f.breaks) {
-      f.write(h);
+    };
+    if (f.breaks || f.ends) {
+      const Vec<CH> v = f.waiting_runs(h);
+      hand_on(last_known ? last : v);
     } else {
+      if (t.info & kInfoBreak) hand_on(past(warp, h));
       T* y = a.y + (size_t)t0 * a.C + ch;
       const int rest = f.on ? a.t.N - t0 : 0;          // tokens to write
 #pragma unroll 4
       for (int q = 0; q < kWarpTokens; ++q, y += a.C) {
-        const Vec<CH> v = rows.mapped(q, h);
-        if (q < rest) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(v);
+        h = rows.step(q, h);
+        if (q < rest) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
       }
     }
-    warp_arrive(&sh.done[t.s]);
-    if (warp == 0 && !serial && (t.info & kInfoSource)) {      // breaks elsewhere start from nodes that end here
-      if (!wait_phase(&sh.done[t.s], t.parity, wc)) return;
-      publish(flag);
+    if (!serial && (t.info & kInfoSource)) {           // breaks elsewhere start from nodes that end here
+      warp_arrive(&g.own);
+      if (!wait_phase(&g.own, n_own & 1, wc)) return;
+      ++n_own;
+      if (warp == 0) publish(flag);
     }
     warp_arrive(&sh.empty[t.s]);
   }
 }
 
-// The mapping warps, backward: p, and the 16-token maps of h and of the gradient (which share the factor).
-template <typename T, int KIND, int GROUPS>
-DEVI void bwd_map(ScanShared<kSlots>& sh, ScanBack<kSlots>& back, uint8_t* slots, int group, int warp,
-                  const WaitCtl& wc) {
+// The mapping warps, backward: p, and the 8-token maps of h and of the gradient (which share the factor).
+template <typename T, int KIND>
+DEVI void bwd_map(BwdShared& sh, ScanBack& back, uint8_t* slots, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH;
   Tile t;
-  for (int i = group; next_tile(sh, i, t, wc); i += GROUPS) {
+  for (int i = 0; next_tile(sh, sh.full, i, t, wc); ++i) {
     const Rows<T> rows(slots, t.s, warp);
     Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f), R = vec<CH>(0.f);
 #pragma unroll 4
@@ -961,7 +1006,7 @@ DEVI void bwd_map(ScanShared<kSlots>& sh, ScanBack<kSlots>& back, uint8_t* slots
   }
 }
 
-// Backward, a warp at whose 16 tokens paths break or join.
+// Backward, a warp at whose 8 tokens paths break or join.
 template <typename T, int KIND>
 struct BwdBreaks {
   static constexpr int CH = Lane<T>::CH;
@@ -969,7 +1014,7 @@ struct BwdBreaks {
   const Rows<T>& rows;
   int t0, ch;
   bool on;
-  int from, end, kid, sib, own;            // per lane q < 16, of token t0 + q; own: its node
+  int from, end, kid, sib, own;            // per lane q < 8, of token t0 + q; own: its node
   uint32_t breaks, joins;
   // h before four tokens from g on; h: before token g, and on return behind the four
   DEVI void befores(int g, Vec<CH>& h, Vec<CH> (&b)[4]) const {
@@ -1008,22 +1053,23 @@ struct BwdBreaks {
 
 // The walking warps, backward: h before every token, then the gradients from the last token to the first.
 template <typename T, int KIND>
-DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>& back, uint8_t* slots, int warp,
-                   const WaitCtl& wc) {
+DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk& gr, uint8_t* slots,
+                   int group, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t n_own = 0, n_turn = 0;
   Tile t;
-  for (int i = 0; next_tile(sh, i, t, wc) && tile_info(sh, t, wc); ++i) {
+  for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kBwdWalks) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;
-    const int t0 = t.k * TILE + warp * kWarpTokens;
+    const int t0 = t.k * kTile + warp * kWarpTokens;
     int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
     const bool mapped = t.info & kInfoMapped, serial = t.info & kInfoSerialBack;
     BwdBreaks<T, KIND> f{a, rows, t0, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u};
     const bool on = f.on;
-    Vec<CH> h = ld_state_if(a.states + (size_t)(a.t.n_nodes + t.k - 1) * a.C + ch, on && (t.info & kInfoIn), Vec<CH>());
+    Vec<CH> h = vec<CH>(0.f);
     if (!mapped) {
+      h = ld_state_if(a.states + (size_t)(a.t.n_nodes + t.k - 1) * a.C + ch, on && (t.info & kInfoIn), h);
       bool ok = true;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
         const int j = t0 + lane;
@@ -1033,11 +1079,11 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
         f.sib = a.w.sib[j];
         f.own = a.t.tok_node[j];
         if (f.kid >= 0) {
-          const int tk = a.t.tok_start[f.kid] / TILE;
+          const int tk = a.t.tok_start[f.kid] / kTile;
           if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
         }
         if (ok && f.sib >= 0) {
-          const int tk = a.t.tok_start[f.sib] / TILE;
+          const int tk = a.t.tok_start[f.sib] / kTile;
           if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
         }
       }
@@ -1049,7 +1095,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
       f.joins = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
     }
     const bool slow = f.breaks | f.joins;
-    if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+    if (!wait_phase(mapped ? &sh.known[t.s] : &sh.mapped[t.s], t.parity, wc)) return;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
         Vec<CH> v = vec<CH>(0.f), b[4];
@@ -1071,15 +1117,17 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
         sh_st(back.R[t.s][warp], R);
       }
       if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
-      warp_arrive(&sh.own);
-      if (!wait_phase(&sh.own, n_own & 1, wc)) return;
+      warp_arrive(&gr.own);
+      if (!wait_phase(&gr.own, n_own & 1, wc)) return;
       ++n_own;
     }
-#pragma unroll
-    for (int q = 0; q < kScanWarps - 1; ++q) {
-      if (q >= warp) break;
-      const Vec<CH> qb = sh_ld<CH>(sh.B[t.s][q]);
-      h = (!mapped && sh.reset[t.s][q]) ? qb : vfma(sh_ld<CH>(sh.A[t.s][q]), h, qb);
+    if (mapped) {
+      h = sh_ld<CH>(sh.B[t.s][warp]);
+    } else {
+      for (int q = 0; q < warp; ++q) {
+        const Vec<CH> qb = sh_ld<CH>(sh.B[t.s][q]);
+        h = sh.reset[t.s][q] ? qb : vfma(sh_ld<CH>(sh.A[t.s][q]), h, qb);
+      }
     }
     // h before every fourth token; the others are stepped to again on the way back (16 values a lane would stay in
     // registers only in straight-line code of 15 KB, which the warps' other code would push out of the cache)
@@ -1089,7 +1137,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
         if (q % 4 == 0) sh_st(back.before[warp][q / 4], h);
         h = advance<KIND>(rows.p(q), rows.get(1, q), h);
       }
-      sh_st(back.before[warp][3], h);
+      sh_st(back.before[warp][kWarpTokens / 4 - 1], h);
     } else {
       Vec<CH> b[4];
 #pragma unroll 1
@@ -1099,26 +1147,21 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
       }
     }
     // the gradient behind the warp, as the state before it in the forward
-    Vec<CH> u;
-    if (!serial) {
-      Vec<CH> A = vec<CH>(1.f), R = vec<CH>(0.f);
-      bool fixed = false;
-#pragma unroll
-      for (int q = kScanWarps - 1; q > 0; --q) {
-        if (q <= warp) break;
-        const bool r = !mapped && sh.reset[t.s][q];
-        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]), qr = sh_ld<CH>(back.R[t.s][q]);
-        R = r ? qr : vfma(qa, R, qr);
-        A = A * qa;
-        fixed |= r;
+    if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
+    Vec<CH> u = sh_ld<CH>(sh.in[t.s]);
+    if (mapped) {
+      u = vfma(sh_ld<CH>(sh.A[t.s][warp]), u, sh_ld<CH>(back.R[t.s][warp]));
+    } else if (!serial) {
+      for (int q = kScanWarps - 1; q > warp; --q) {
+        const Vec<CH> qr = sh_ld<CH>(back.R[t.s][q]);
+        u = sh.reset[t.s][q] ? qr : vfma(sh_ld<CH>(sh.A[t.s][q]), u, qr);
       }
-      if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
-      u = fixed ? R : vfma(A, sh_ld<CH>(sh.in[t.s]), R);
     } else {
-      if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
-      if (warp < kScanWarps - 1 && !wait_phase(&sh.turn[warp], n_turn & 1, wc)) return;
+      if (warp < kScanWarps - 1) {
+        if (!wait_phase(&gr.turn[warp], n_turn & 1, wc)) return;
+        u = sh_ld<CH>(gr.carry[warp + 1]);
+      }
       ++n_turn;
-      u = sh_ld<CH>(warp < kScanWarps - 1 ? sh.carry[warp + 1] : sh.in[t.s]);
     }
     // token q: lam = what reaches it; its gradients; u before it
     auto step = [&](int q, Vec<CH> lam, Vec<CH> before) {
@@ -1184,41 +1227,45 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared<kSlots>& sh, ScanBack<kSlots>
     }
     if (!mapped) {
       if (serial && warp > 0) {
-        sh_st(sh.carry[warp], u);
-        warp_arrive(&sh.turn[warp - 1]);
+        sh_st(gr.carry[warp], u);
+        warp_arrive(&gr.turn[warp - 1]);
       }
       if (warp == 0) {
         if (on) hand_state(a.w.carry + (size_t)t.k * a.C + ch, u);
         if (serial) publish(flag);
       }
     }
-    warp_arrive(&sh.done[t.s]);
-    if (warp == 0 && !serial && (t.info & kInfoBreak)) {
-      if (!wait_phase(&sh.done[t.s], t.parity, wc)) return;
-      publish(flag);
+    if (!mapped && !serial && (t.info & kInfoBreak)) {
+      warp_arrive(&gr.own);
+      if (!wait_phase(&gr.own, n_own & 1, wc)) return;
+      ++n_own;
+      if (warp == 0) publish(flag);
     }
     warp_arrive(&sh.empty[t.s]);
   }
 }
 
-constexpr int kScanSmem = kSlots * kPlanes * kPlane + 1024;
+constexpr int scan_smem(int slots) { return slots * kPlanes * kPlane + 128; }
 
-DEVI uint8_t* scan_align(uint8_t* p) { return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u); }
+DEVI uint8_t* scan_align(uint8_t* p) { return p + ((128u - (smem_u32(p) & 127u)) & 127u); }   // copies land on 128 bytes
 
-DEVI void scan_init(ScanShared<kSlots>& sh) {
+template <int SLOTS, int MAPS, int WALKS>
+DEVI void scan_init(ScanShared<SLOTS, MAPS>& sh, ScanWalk (&walks)[WALKS]) {
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(&sh.drawn[s], 1);
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.told[s], 1);
-      mbar_init(&sh.mapped[s], kScanWarps);
+      mbar_init(&sh.mapped[s], kScanWarps * MAPS);
       mbar_init(&sh.known[s], 1);
-      mbar_init(&sh.done[s], kScanWarps);
       mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], kScanWarps + 1);     // the walking warps and the joining warp
     }
-    mbar_init(&sh.own, kScanWarps);
-    for (int q = 0; q < kScanWarps; ++q) mbar_init(&sh.turn[q], 1);
+    for (int g = 0; g < WALKS; ++g) {
+      mbar_init(&walks[g].own, kScanWarps);
+      for (int q = 0; q < kScanWarps; ++q) mbar_init(&walks[g].turn[q], 1);
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -1227,62 +1274,70 @@ DEVI void scan_init(ScanShared<kSlots>& sh) {
 // Every wait between warps is on an mbarrier and has a limit; the first that gives up raises the block's
 // abort flag, which ends the others.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(scan_threads(kFwdGroups), 1) k_scan_fwd(const __grid_constant__ CUtensorMap tm_gate,
+__global__ void __launch_bounds__(scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), 1) k_scan_fwd(const __grid_constant__ CUtensorMap tm_gate,
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const ScanFwd<T> a) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ScanShared<kSlots> sh;
-  __shared__ ScanEnds kept;
+  __shared__ FwdShared sh;
+  __shared__ ScanWalk walks[kFwdWalks];
+  __shared__ ScanEnds kept[kFwdWalks];
   uint8_t* slots = scan_align(smem_raw);
-  scan_init(sh);
+  scan_init(sh, walks);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  constexpr int WALK = kFwdGroups * kScanWarps, LOAD = WALK + kScanWarps;     // first warp of each role
+  constexpr int WALK = kFwdMaps * kScanWarps, LOAD = WALK + kFwdWalks * kScanWarps;     // first warp of each role
   const int warp = threadIdx.x >> 5;
   if (warp < WALK) {
-    fwd_map<T, KIND, kFwdGroups>(sh, slots, warp / kScanWarps, warp % kScanWarps, wc);
+    fwd_map<T, KIND>(sh, slots, warp, wc);
   } else if (warp < LOAD) {
-    fwd_walk<T, KIND>(a, sh, kept, slots, warp - WALK, wc);
+    const int group = warp / kScanWarps - kFwdMaps;
+    fwd_walk<T>(a, sh, walks[group], kept[group], slots, group, warp % kScanWarps, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
-    scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, false, wc);
+    scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
   } else if (warp == LOAD + 1) {
-    scan_publish<true, CH>(sh, sh.B, a.w, a.C, SLAB, wc);
+    fwd_publish<CH>(sh, a.w, a.C, SLAB, wc);
   } else {
-    scan_join<true, CH>(sh, a.w, a.C, a.states + (size_t)a.t.n_nodes * a.C, SLAB, warp - LOAD - 2, wc);
+    scan_join<true, CH, kFwdJoins>(sh, a.w, a.C, a.t.n_tiles, a.states + (size_t)a.t.n_nodes * a.C, SLAB, false,
+                                   warp - LOAD - 2, wc);
   }
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(scan_threads(kBwdGroups), 1) k_scan_bwd(const __grid_constant__ CUtensorMap tm_gate,
+__global__ void __launch_bounds__(scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), 1) k_scan_bwd(const __grid_constant__ CUtensorMap tm_gate,
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const __grid_constant__ CUtensorMap tm_dy,
                                                               const ScanBwd<T> a) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ScanShared<kSlots> sh;
-  __shared__ ScanBack<kSlots> back;
+  __shared__ BwdShared sh;
+  __shared__ ScanBack back;
+  __shared__ ScanWalk walks[kBwdWalks];
   uint8_t* slots = scan_align(smem_raw);
-  scan_init(sh);
+  scan_init(sh, walks);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  constexpr int WALK = kBwdGroups * kScanWarps, LOAD = WALK + kScanWarps;     // first warp of each role
+  constexpr int WALK = kBwdMaps * kScanWarps, LOAD = WALK + kBwdWalks * kScanWarps;     // first warp of each role
   const int warp = threadIdx.x >> 5;
   if (warp < WALK) {
-    bwd_map<T, KIND, kBwdGroups>(sh, back, slots, warp / kScanWarps, warp % kScanWarps, wc);
+    bwd_map<T, KIND>(sh, back, slots, warp, wc);
   } else if (warp < LOAD) {
-    bwd_walk<T, KIND>(a, sh, back, slots, warp - WALK, wc);
+    const int group = warp / kScanWarps - kBwdMaps;
+    bwd_walk<T, KIND>(a, sh, back, walks[group], slots, group, warp % kScanWarps, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[3] = {&tm_gate, &tm_x, &tm_dy};
-    scan_load<false>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, a.d_final != nullptr, wc);
+    scan_load<false>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
   } else if (warp == LOAD + 1) {
-    scan_publish<false, CH>(sh, back.R, a.w, a.C, SLAB, wc);
+    bwd_publish<CH>(sh, back, a.w, a.states + (size_t)a.t.n_nodes * a.C, a.C, SLAB, wc);
   } else {
-    scan_join<false, CH>(sh, a.w, a.C, a.w.carry, SLAB, warp - LOAD - 2, wc);
+    scan_join<false, CH, kBwdJoins>(sh, a.w, a.C, a.t.n_tiles, a.w.carry, SLAB, a.d_final != nullptr,
+                                    warp - LOAD - 2, wc);
   }
 }
 
 // ---------------------------------------------------------------------------------------------
 // host side
+
+int scan_tiles(const tree_plan_t* p) { return (int)(((int64_t)p->n_tokens + kTile - 1) / kTile); }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
@@ -1298,7 +1353,7 @@ struct ScanLayout {
 
 ScanLayout scan_layout(const tree_plan_t* p, int C) {
   ScanLayout L{};
-  const size_t tok = align256((size_t)p->n_tokens * 4), tiles = (size_t)p->n_tiles;
+  const size_t tok = align256((size_t)p->n_tokens * 4), tiles = (size_t)scan_tiles(p);
   size_t o = 0;
   L.link = o;  o += tok;
   L.end = o;   o += tok;
@@ -1336,18 +1391,18 @@ int scan_args(const tree_plan_t* plan, const int32_t* parent, const int32_t* nod
 
 ScanTree scan_tree(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len) {
   return ScanTree{plan->tok_node, plan->tok_start, plan->sub_end, parent, node_len,
-                  plan->n_tokens, plan->n_nodes,   plan->n_tiles};
+                  plan->n_tokens, plan->n_nodes,   scan_tiles(plan)};
 }
 
-// a tensor [N][C] in boxes of 128 tokens by a slab's channels; what lies outside reads as zero
+// a tensor [N][C] in boxes of 64 tokens by a slab's channels; what lies outside reads as zero
 template <typename T>
 int scan_map(CUtensorMap* m, const void* base, int C, int N) {
   constexpr int box = kRow / (int)sizeof(T);
-  return sizeof(T) == 2 ? make_tmap_bf16_2d(m, base, C, N, box, TILE) : make_tmap_f32_2d(m, base, C, N, box, TILE);
+  return sizeof(T) == 2 ? make_tmap_bf16_2d(m, base, C, N, box, kTile) : make_tmap_f32_2d(m, base, C, N, box, kTile);
 }
 
 // A block an SM, or one for each unit of work.  The kernel's shared memory is announced once a device.
-template <auto KERN>
+template <auto KERN, int SMEM>
 int scan_grid(int64_t units, unsigned* blocks) {
   static std::atomic<int> sms_of[64];              // one array a kernel; 0: not announced yet
   int dev = 0, sms = 0;
@@ -1355,7 +1410,7 @@ int scan_grid(int64_t units, unsigned* blocks) {
   if (rc) return rc;
   if (dev < 64) sms = sms_of[dev].load(std::memory_order_acquire);
   if (!sms) {
-    rc = record_cuda(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, kScanSmem));
+    rc = record_cuda(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
     if (!rc) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
     if (rc) return rc;
     if (dev < 64) sms_of[dev].store(sms, std::memory_order_release);
@@ -1370,17 +1425,17 @@ dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (
 template <typename T, int KIND>
 int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, cudaStream_t s) {
   unsigned blocks = 0;
-  const int rc = scan_grid<&k_scan_fwd<T, KIND>>((int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_fwd<T, KIND>, scan_smem(kFwdSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdGroups), kScanSmem, s>>>(tg, tx, a);
+  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), scan_smem(kFwdSlots), s>>>(tg, tx, a);
   return record_cuda(cudaGetLastError());
 }
 template <typename T, int KIND>
 int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, const CUtensorMap& td, cudaStream_t s) {
   unsigned blocks = 0;
-  const int rc = scan_grid<&k_scan_bwd<T, KIND>>((int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_bwd<T, KIND>, scan_smem(kBwdSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdGroups), kScanSmem, s>>>(tg, tx, td, a);
+  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), scan_smem(kBwdSlots), s>>>(tg, tx, td, a);
   return record_cuda(cudaGetLastError());
 }
 
@@ -1392,8 +1447,8 @@ int scan_fwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<prepare_grid(t, C), TILE, 0, s>>>(t, w, slabs, C, 0, states, states + (size_t)t.n_nodes * C);
-  const ScanFwd<T> a{static_cast<const T*>(gate), static_cast<const T*>(x), init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
+  k_scan_prepare<<<prepare_grid(t, C), kTile, 0, s>>>(t, w, slabs, C, 0, states, states + (size_t)t.n_nodes * C);
+  const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_fwd<T, TREE_GATE_SIGMOID>(a, tg, tx, s)
                                    : run_fwd<T, TREE_GATE_LOG>(a, tg, tx, s);
 }
@@ -1408,7 +1463,7 @@ int scan_bwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (!rc) rc = scan_map<T>(&td, dy, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<prepare_grid(t, C), TILE, 0, s>>>(t, w, slabs, C, 1, d_init, w.carry);
+  k_scan_prepare<<<prepare_grid(t, C), kTile, 0, s>>>(t, w, slabs, C, 1, d_init, w.carry);
   const ScanBwd<T> a{init, states, d_final, static_cast<T*>(dgate), static_cast<T*>(dx), d_init, t, w, C, slabs, status,
                      wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_bwd<T, TREE_GATE_SIGMOID>(a, tg, tx, td, s)
@@ -1421,6 +1476,11 @@ int scan_bwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
 using namespace ta;
 
 extern "C" {
+
+int64_t tree_scan_rows(const tree_plan_t* plan) {
+  if (!plan || plan->n_tokens <= 0 || plan->n_nodes <= 0) return 0;
+  return (int64_t)plan->n_nodes + scan_tiles(plan);
+}
 
 size_t tree_scan_workspace(const tree_plan_t* plan, int C) {
   if (!plan || plan->n_tokens <= 0 || plan->n_nodes <= 0 || C <= 0) return 0;
