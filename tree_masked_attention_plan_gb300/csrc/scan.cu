@@ -476,13 +476,23 @@ using FwdShared = ScanShared<kFwdSlots, kFwdMaps>;
 using BwdShared = ScanShared<kBwdSlots, kBwdMaps>;
 // A group of walking warps among themselves.
 struct ScanWalk {
-  uint64_t own, turn[kScanWarps];                  // their own maps are there (all wait); the warp before is through
+  uint64_t own, turn[kScanWarps];                  // all of them are here; carry of the warp before is there
   alignas(16) float carry[kScanWarps][64];         // the state before (gradient behind) a warp, where they go one by one
+  // The last such tile (counted from 1) in which token i's row (forward: the state of the node that ends there,
+  // backward: the gradient that the node that starts there hands on) was written: warps of one tile wait for it.
+  int row_of[kTile];
 };
 struct ScanBack {
   alignas(16) float R[kBwdSlots][kScanWarps][64];      // the gradient's map is u -> A u + R
   alignas(16) float before[kScanWarps][kWarpTokens / 4][64];     // h before every fourth token, where it cannot stay in registers
 };
+
+// the warp's row of token tok (and what it wrote before) is there for the other warps of the block
+DEVI void row_written(ScanWalk& walk, int tok, int serial) {
+  __threadfence_block();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) *(volatile int*)&walk.row_of[tok] = serial;
+}
 
 // Forward: the states behind nodes that end in the tile at hand, one for every kKeep tokens (the last that came).
 constexpr int kKeep = 8;
@@ -804,9 +814,11 @@ struct FwdRuns {
   static constexpr int CH = Lane<T>::CH;
   const ScanFwd<T>& a;
   const Rows<T>& rows;
+  ScanWalk& walk;
   ScanEnds& kept;
   int k, t0, ch;
   bool on;
+  int serial;                              // the tile's number among those whose warps go one by one, 0: it is none
   int from, end;                           // per lane q < 8: link of token t0 + q, its node if it is the node's last
   uint32_t breaks, ends, reset;            // a bit a token; reset: breaks that start from outside the tile
   DEVI uint32_t behind(int q) const { return q < 31 ? ~((2u << q) - 1u) : 0u; }
@@ -818,15 +830,30 @@ struct FwdRuns {
   DEVI Vec<CH> run(Vec<CH> h, int q0) const {
     const int q1 = run_end(q0);
 #pragma unroll 1
-    for (int q = q0; q < q1; ++q) {
-      h = rows.step(q, h);
-      if (on && t0 + q < a.t.N) *reinterpret_cast<uint32_t*>(a.y + (size_t)(t0 + q) * a.C + ch) = Lane<T>::pack(h);
-      if ((ends >> q) & 1u) {              // a node's last token: its state, for the user and for breaks
-        const int e = __shfl_sync(0xffffffffu, end, q), tok = t0 + q - k * kTile, slot = tok / kKeep;
-        if (on) st_state(a.states + (size_t)e * a.C + ch, h);
-        sh_st(kept.state[slot], h);
-        if ((threadIdx.x & 31) == 0) kept.token[slot] = tok;
-        __syncwarp();
+    while (q0 < q1) {
+      const uint32_t m = ends >> q0;
+      const int e = m ? q0 + __ffs(m) - 1 : kWarpTokens, stop = min(e + 1, q1);
+      T* y = a.y + (size_t)(t0 + q0) * a.C + ch;
+      const int rest = on ? a.t.N - t0 : 0;
+#pragma unroll 4
+      for (; q0 < stop; ++q0, y += a.C) {
+        h = rows.step(q0, h);
+        if (q0 < rest) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
+      }
+      if (e < q1) {                        // a node's last token: its state, for the user and for breaks
+        const int n = __shfl_sync(0xffffffffu, end, e), tok = t0 + e - k * kTile, slot = tok / kKeep;
+        if (on) st_state(a.states + (size_t)n * a.C + ch, h);
+        if (serial) {
+          // no token's while it changes: whoever reads it looks at the token afterwards
+          if ((threadIdx.x & 31) == 0) *(volatile int*)&kept.token[slot] = -1;
+          __threadfence_block();
+          __syncwarp();
+          sh_st(kept.state[slot], h);
+          __threadfence_block();
+          __syncwarp();
+          if ((threadIdx.x & 31) == 0) *(volatile int*)&kept.token[slot] = tok;
+          row_written(walk, tok, serial);
+        }
       }
     }
     return h;
@@ -858,19 +885,27 @@ struct FwdRuns {
     }
     return reset && (breaks >> (31 - __clz(reset))) == 1u;
   }
-  // The runs that wait: the one that comes into the warp, and those that start from nodes of this tile.  Returns
-  // the state behind the last of them.
-  DEVI Vec<CH> waiting_runs(Vec<CH> h) const {
+  // The runs that wait: the one that comes into the warp, and those that start from nodes of this tile.  v: the
+  // state behind the last of them; false if a wait gave up.
+  DEVI bool waiting_runs(Vec<CH> h, Vec<CH>& v, const WaitCtl& wc) const {
     if (!(breaks & 1u)) h = run(h, 0);
 #pragma unroll 1
     for (uint32_t m = breaks & ~reset; m; m &= m - 1) {
       const int q = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, from, q);
       const int tok = a.t.tok_start[n] + a.t.node_len[n] - 1 - k * kTile, slot = tok / kKeep;
-      // kept, unless the end of another node within the same tokens has taken its place
-      h = kept.token[slot] == tok ? sh_ld<CH>(kept.state[slot]) : ld_state_if(a.states + (size_t)n * a.C + ch, on, h);
+      const bool ok = wait_until([&] { return *(volatile int*)&walk.row_of[tok] == serial; }, wc, a.w.ctl + 2);
+      if (!__all_sync(0xffffffffu, ok)) return false;
+      __threadfence_block();
+      // kept, unless the end of another node within the same tokens has taken its place (looked at twice: the
+      // other one may come meanwhile)
+      const Vec<CH> near = sh_ld<CH>(kept.state[slot]);
+      __threadfence_block();
+      const bool here = __all_sync(0xffffffffu, *(volatile int*)&kept.token[slot] == tok);
+      h = here ? near : ld_state_if(a.states + (size_t)n * a.C + ch, on, h);
       h = run(h, q);
     }
-    return h;
+    v = h;
+    return true;
   }
 };
 
@@ -880,14 +915,17 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
                    int group, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
-  uint32_t n_own = 0, n_turn = 0;                      // uses of the walking warps' barriers so far
+  uint32_t n_own = 0;                                  // uses of the walking warps' barriers so far
+  int n_turn = 0;
   Tile t;
   for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kFwdWalks) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;          // the lane's first channel
     const int t0 = t.k * kTile + warp * kWarpTokens;
-    FwdRuns<T> f{a, rows, kept, t.k, t0, ch, ch < a.C, kLinkChain, -1, 0u, 0u, 0u};
-    const bool serial = t.info & kInfoSerial, special = t.info & (kInfoBreak | kInfoEnd);
+    const bool serial = t.info & kInfoSerial;
+    n_turn += serial;
+    FwdRuns<T> f{a, rows, g, kept, t.k, t0, ch, ch < a.C, serial ? n_turn : 0, kLinkChain, -1, 0u, 0u, 0u};
+    const bool special = t.info & (kInfoBreak | kInfoEnd);
     if (special) {
       bool ok = true, tile = false;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
@@ -912,7 +950,6 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
     if (t.info & kInfoBreak) {
       if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
       if (serial) {                                    // no warp is a tile ahead, where its turn would overtake this one's
-        if (lane < kTile / kKeep / kScanWarps) kept.token[warp * (kTile / kKeep / kScanWarps) + lane] = -1;
         warp_arrive(&g.own);
         if (!wait_phase(&g.own, n_own & 1, wc)) return;
         ++n_own;
@@ -934,35 +971,34 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
         v = vfma(sh_ld<CH>(sh.A[t.s][q * kFwdMaps + m]), v, sh_ld<CH>(sh.B[t.s][q * kFwdMaps + m]));
       return v;
     };
+    auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles behind
+      if (serial && warp < kScanWarps - 1) {
+        sh_st(g.carry[warp], v);
+        warp_arrive(&g.turn[warp + 1]);
+      }
+      if (warp == kScanWarps - 1 && f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
+    };
+    if (last_known) hand_on(last);
     if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
     Vec<CH> h = sh_ld<CH>(sh.in[t.s]);
     if (t.info & kInfoMapped) {
       h = vfma(sh_ld<CH>(sh.A[t.s][warp * kFwdMaps]), h, sh_ld<CH>(sh.B[t.s][warp * kFwdMaps]));
     } else if (!serial) {
       for (int q = 0; q < warp; ++q) h = sh.reset[t.s][q] ? sh_ld<CH>(sh.B[t.s][q * kFwdMaps]) : past(q, h);
-    } else {
-      if (warp > 0) {
-        if (!wait_phase(&g.turn[warp], n_turn & 1, wc)) return;
-        h = sh_ld<CH>(g.carry[warp - 1]);
-      }
-      ++n_turn;
+    } else if (warp > 0) {
+      if (!wait_phase(&g.turn[warp], (n_turn - 1) & 1, wc)) return;
+      h = sh_ld<CH>(g.carry[warp - 1]);
     }
-    int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
-    auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles behind
-      if (serial && warp < kScanWarps - 1) {
-        sh_st(g.carry[warp], v);
-        warp_arrive(&g.turn[warp + 1]);
-      }
-      if ((t.info & kInfoBreak) && warp == kScanWarps - 1) {
-        if (f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
-        if (serial) publish(flag);
-      }
-    };
+    // a warp without breaks hands on by its maps, before it walks
+    if ((t.info & kInfoBreak) && !f.breaks) hand_on(past(warp, h));
     if (f.breaks || f.ends) {
-      const Vec<CH> v = f.waiting_runs(h);
-      hand_on(last_known ? last : v);
+      Vec<CH> v;
+      if (!f.waiting_runs(h, v, wc)) {
+        if (lane == 0) sh.abort_flag = 1;
+        return;
+      }
+      if (f.breaks && !last_known) hand_on(v);
     } else {
-      if (t.info & kInfoBreak) hand_on(past(warp, h));
       T* y = a.y + (size_t)t0 * a.C + ch;
       const int rest = f.on ? a.t.N - t0 : 0;          // tokens to write
 #pragma unroll 4
@@ -971,11 +1007,11 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
         if (q < rest) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
       }
     }
-    if (!serial && (t.info & kInfoSource)) {           // breaks elsewhere start from nodes that end here
+    if (t.info & kInfoSource) {                        // breaks elsewhere start from nodes that end here
       warp_arrive(&g.own);
       if (!wait_phase(&g.own, n_own & 1, wc)) return;
       ++n_own;
-      if (warp == 0) publish(flag);
+      if (warp == 0) publish(a.w.flags + (size_t)t.k * a.slabs + t.slab);
     }
     warp_arrive(&sh.empty[t.s]);
   }
@@ -1016,6 +1052,7 @@ struct BwdBreaks {
   bool on;
   int from, end, kid, sib, own;            // per lane q < 8, of token t0 + q; own: its node
   uint32_t breaks, joins;
+  int kid_at, sib_at;                      // per lane: the token of this tile at which kid, sib starts; -1: in another
   // h before four tokens from g on; h: before token g, and on return behind the four
   DEVI void befores(int g, Vec<CH>& h, Vec<CH> (&b)[4]) const {
     if ((breaks >> g) & 15u) {
@@ -1057,7 +1094,8 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
                    int group, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
-  uint32_t n_own = 0, n_turn = 0;
+  uint32_t n_own = 0;
+  int n_turn = 0;
   Tile t;
   for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kBwdWalks) {
     const Rows<T> rows(slots, t.s, warp);
@@ -1065,7 +1103,8 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
     const int t0 = t.k * kTile + warp * kWarpTokens;
     int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
     const bool mapped = t.info & kInfoMapped, serial = t.info & kInfoSerialBack;
-    BwdBreaks<T, KIND> f{a, rows, t0, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u};
+    BwdBreaks<T, KIND> f{a, rows, t0, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u, -1, -1};
+    n_turn += serial;
     const bool on = f.on;
     Vec<CH> h = vec<CH>(0.f);
     if (!mapped) {
@@ -1081,10 +1120,12 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
         if (f.kid >= 0) {
           const int tk = a.t.tok_start[f.kid] / kTile;
           if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
+          else f.kid_at = a.t.tok_start[f.kid] - t.k * kTile;
         }
         if (ok && f.sib >= 0) {
           const int tk = a.t.tok_start[f.sib] / kTile;
           if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
+          else f.sib_at = a.t.tok_start[f.sib] - t.k * kTile;
         }
       }
       if (!__all_sync(0xffffffffu, ok)) {
@@ -1095,6 +1136,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
       f.joins = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
     }
     const bool slow = f.breaks | f.joins;
+    const bool near = __any_sync(0xffffffffu, f.kid_at >= 0);         // a node of this tile joins in the warp
     if (!wait_phase(mapped ? &sh.known[t.s] : &sh.mapped[t.s], t.parity, wc)) return;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
@@ -1103,7 +1145,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
         for (int g = 0; g < kWarpTokens; g += 4) f.befores(g, v, b);
         sh_st(sh.B[t.s][warp], v);
       }
-      if (slow && !serial) {
+      if (slow && !near) {
         Vec<CH> R = vec<CH>(0.f), d[4];
 #pragma unroll 1
         for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
@@ -1147,6 +1189,14 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
       }
     }
     // the gradient behind the warp, as the state before it in the forward
+    auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles before
+      if (serial && warp > 0) {
+        sh_st(gr.carry[warp], v);
+        warp_arrive(&gr.turn[warp - 1]);
+      }
+      if (warp == 0 && on) hand_state(a.w.carry + (size_t)t.k * a.C + ch, v);
+    };
+    if (f.breaks && !near) hand_on(sh_ld<CH>(back.R[t.s][warp]));
     if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
     Vec<CH> u = sh_ld<CH>(sh.in[t.s]);
     if (mapped) {
@@ -1156,13 +1206,18 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
         const Vec<CH> qr = sh_ld<CH>(back.R[t.s][q]);
         u = sh.reset[t.s][q] ? qr : vfma(sh_ld<CH>(sh.A[t.s][q]), u, qr);
       }
-    } else {
-      if (warp < kScanWarps - 1) {
-        if (!wait_phase(&gr.turn[warp], n_turn & 1, wc)) return;
-        u = sh_ld<CH>(gr.carry[warp + 1]);
-      }
-      ++n_turn;
+    } else if (warp < kScanWarps - 1) {
+      if (!wait_phase(&gr.turn[warp], (n_turn - 1) & 1, wc)) return;
+      u = sh_ld<CH>(gr.carry[warp + 1]);
     }
+    // a warp in which nothing of this tile joins hands on by its map, before it walks
+    if (!mapped && !f.breaks && !near) hand_on(vfma(sh_ld<CH>(sh.A[t.s][warp]), u, sh_ld<CH>(back.R[t.s][warp])));
+    bool ok = true;
+    auto wait_row = [&](int tok) {                     // of a node that starts in this tile
+      const bool there = wait_until([&] { return *(volatile int*)&gr.row_of[tok] == n_turn; }, wc, a.w.ctl + 2);
+      ok = __all_sync(0xffffffffu, there) && ok;
+      __threadfence_block();
+    };
     // token q: lam = what reaches it; its gradients; u before it
     auto step = [&](int q, Vec<CH> lam, Vec<CH> before) {
       const Vec<CH> p = rows.p(q);
@@ -1202,6 +1257,10 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
       for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
         Vec<CH> b[4], d[4], hg = sh_ld<CH>(back.before[warp][g / 4]);
         f.befores(g, hg, b);
+        for (uint32_t m = near ? (f.joins >> g) & 15u : 0u; m; m &= m - 1) {
+          const int at = __shfl_sync(0xffffffffu, f.kid_at, g + __ffs(m) - 1);
+          if (at >= 0 && (at - warp * kWarpTokens) / 4 != g / 4) wait_row(at);      // (those of these four: below)
+        }
         f.sums(g, d);
 #pragma unroll
         for (int q = 3; q >= 0; --q) {
@@ -1217,25 +1276,23 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
           if ((f.breaks >> (g + q)) & 1u) {            // what this path hands to the state it started from
             const int n = __shfl_sync(0xffffffffu, f.from, g + q), v = __shfl_sync(0xffffffffu, f.own, g + q);
             const int sb = __shfl_sync(0xffffffffu, f.sib, g + q);
+            const int sb_at = __shfl_sync(0xffffffffu, f.sib_at, g + q);
+            if (sb_at >= 0) wait_row(sb_at);
             const Vec<CH> later = ld_state_if(a.w.dnode + (size_t)sb * a.C + ch, on && sb >= 0, u);
             if (on && n >= 0) st_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
             if (on && n == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
             u = vec<CH>(0.f);
+            if (serial) row_written(gr, warp * kWarpTokens + g + q, n_turn);
           }
         }
       }
     }
-    if (!mapped) {
-      if (serial && warp > 0) {
-        sh_st(gr.carry[warp], u);
-        warp_arrive(&gr.turn[warp - 1]);
-      }
-      if (warp == 0) {
-        if (on) hand_state(a.w.carry + (size_t)t.k * a.C + ch, u);
-        if (serial) publish(flag);
-      }
+    if (!ok) {
+      if (lane == 0) sh.abort_flag = 1;
+      return;
     }
-    if (!mapped && !serial && (t.info & kInfoBreak)) {
+    if (near) hand_on(u);
+    if (!mapped && (t.info & kInfoBreak)) {
       warp_arrive(&gr.own);
       if (!wait_phase(&gr.own, n_own & 1, wc)) return;
       ++n_own;
@@ -1263,6 +1320,7 @@ DEVI void scan_init(ScanShared<SLOTS, MAPS>& sh, ScanWalk (&walks)[WALKS]) {
       mbar_init(&sh.empty[s], kScanWarps + 1);     // the walking warps and the joining warp
     }
     for (int g = 0; g < WALKS; ++g) {
+      for (int q = 0; q < kTile; ++q) walks[g].row_of[q] = 0;
       mbar_init(&walks[g].own, kScanWarps);
       for (int q = 0; q < kScanWarps; ++q) mbar_init(&walks[g].turn[q], 1);
     }
