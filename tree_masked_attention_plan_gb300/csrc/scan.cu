@@ -1392,6 +1392,121 @@ __global__ void __launch_bounds__(scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), 
   }
 }
 
+// Forward for at most a tile of tokens (a decoding step): one launch, a block a slab, no maps and nothing to
+// wait for.  Latency is all: the gates and inputs of a warp's eight tokens are on their way while lanes 0-7
+// find out where these start from; then each warp walks the trees that begin within its eight tokens to
+// their ends.  By 4096 bf16 channels: 64 one-token nodes in 4.6 us (20.6 by the kernels for many tokens), 128 in
+// 5.5 (22), a chain of 128 in 6.3 (10.4), a chain of 64 with 64 one-token children in 14 (52).
+constexpr int kStepWarps = 16, kStepTokens = kTile / kStepWarps;
+template <typename T>
+constexpr int step_smem(int N) { return (N + kStepTokens - 1) / kStepTokens * kStepTokens * 2 * 32 * Lane<T>::CH * 4; }
+
+template <typename T, int KIND>
+__global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, const T* x, const ScanFwd<T> a) {
+  constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
+  extern __shared__ float step_rows[];                 // per token: its decays, its inputs (its states once walked)
+  __shared__ int from[kTile], node[kTile];             // where a break's state lies, the token's node
+  __shared__ uint32_t bits[kStepWarps][3];             // per warp's tokens: roots' first, breaks, nodes' last
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.t.N;
+  const int ch = blockIdx.x * SLAB + lane * CH, t0 = warp * kStepTokens, j = t0 + lane;
+  const bool on = ch < a.C;
+  auto decay = [&](int j) { return step_rows + j * 2 * 32 * CH; };
+  auto input = [&](int j) { return step_rows + (j * 2 + 1) * 32 * CH; };
+  uint32_t gw[kStepTokens], xw[kStepTokens];
+#pragma unroll
+  for (int q = 0; q < kStepTokens; ++q) {
+    const size_t at = (size_t)(t0 + q) * a.C + ch;
+    const bool in = on && t0 + q < N;
+    gw[q] = in ? __ldg(reinterpret_cast<const uint32_t*>(gate + at)) : 0u;
+    xw[q] = in ? __ldg(reinterpret_cast<const uint32_t*>(x + at)) : 0u;
+  }
+  int start = kLinkChain, own = 0;
+  bool last = false;
+  if (lane < kStepTokens && j < N) {
+    own = a.t.tok_node[j];
+    const int first = a.t.tok_start[own], len = a.t.node_len[own];
+    const int up = j == first ? scan_token_ancestor(own, a.t) : -1;
+    const int src = up < 0 ? -1 : a.t.tok_start[up] + a.t.node_len[up] - 1;
+    if (j == first) start = src < 0 || src >= j ? kLinkRoot : src == j - 1 ? kLinkChain : up;
+    last = j == first + len - 1;
+    from[j] = src;
+    node[j] = own;
+  }
+  const uint32_t roots = __ballot_sync(0xffffffffu, start == kLinkRoot);
+  const uint32_t breaks = __ballot_sync(0xffffffffu, start != kLinkChain), ends = __ballot_sync(0xffffffffu, last);
+  if (lane == 0) {
+    bits[warp][0] = roots;
+    bits[warp][1] = breaks;
+    bits[warp][2] = ends;
+  }
+  // a root's input takes its initial state in: h = a init + b
+  Vec<CH> h0[kStepTokens];
+#pragma unroll
+  for (int q = 0; q < kStepTokens; ++q) {
+    const int v = __shfl_sync(0xffffffffu, own, q);
+    h0[q] = ld_state_if(a.init + (size_t)v * a.C + ch, on && a.init && ((roots >> q) & 1u), vec<CH>(0.f));
+  }
+#pragma unroll
+  for (int q = 0; q < kStepTokens; ++q) {
+    if (t0 + q >= N) break;
+    Vec<CH> d, b;
+    token_of<KIND>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
+    if ((roots >> q) & 1u) b = vfma(d, h0[q], b);
+    sh_st(decay(t0 + q), d);
+    sh_st(input(t0 + q), b);
+  }
+  // rows of nodes without tokens
+  for (int v0 = warp * 32; v0 < a.t.n_nodes; v0 += kStepWarps * 32) {
+    const int v = v0 + lane;
+    uint32_t m = __ballot_sync(0xffffffffu, v < a.t.n_nodes && a.t.node_len[min(v, a.t.n_nodes - 1)] <= 0);
+    for (; m; m &= m - 1)
+      if (on) st_state(a.states + (size_t)(v0 + __ffs(m) - 1) * a.C + ch, vec<CH>(0.f));
+  }
+  __syncthreads();
+  if (!roots) return;
+  Vec<CH> h = vec<CH>(0.f);
+  int q0 = __ffs(roots) - 1;
+#pragma unroll 1
+  for (int w = warp; w * kStepTokens < N; ++w, q0 = 0) {
+    const uint32_t rt = bits[w][0], br = bits[w][1], en = bits[w][2];
+    const int at = w * kStepTokens, q1 = min(w > warp && rt ? __ffs(rt) - 1 : kStepTokens, N - at);
+    Vec<CH> d[kStepTokens], b[kStepTokens];
+    int src[kStepTokens];
+#pragma unroll
+    for (int q = 0; q < kStepTokens; ++q) {
+      d[q] = sh_ld<CH>(decay(at + q));
+      b[q] = sh_ld<CH>(input(at + q));
+      src[q] = from[at + q];
+    }
+    T* y = a.y + (size_t)at * a.C + ch;
+    if (!br && q1 == kStepTokens) {                    // (no branch between the tokens: a chain of 128 by 4096 in 6.3 us, else 13.3)
+#pragma unroll
+      for (int q = 0; q < kStepTokens; ++q, y += a.C) {
+        h = vfma(d[q], h, b[q]);
+        b[q] = h;
+        if (on) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
+      }
+#pragma unroll
+      for (int q = 0; q < kStepTokens; ++q) sh_st(input(at + q), b[q]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < kStepTokens; ++q, y += a.C) {
+        if (q < q0 || q >= q1) continue;
+        if ((br >> q) & 1u) h = (rt >> q) & 1u ? vec<CH>(0.f) : sh_ld<CH>(input(src[q]));
+        h = vfma(d[q], h, b[q]);
+        sh_st(input(at + q), h);
+        if (on) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
+      }
+    }
+    for (uint32_t m = en & ~((1u << q0) - 1u) & ((1u << q1) - 1u); m; m &= m - 1) {
+      const int q = at + __ffs(m) - 1;
+      if (on) st_state(a.states + (size_t)node[q] * a.C + ch, sh_ld<CH>(input(q)));
+    }
+    if (w > warp && rt) return;
+  }
+  if (on && N == kTile) st_state(a.states + (size_t)a.t.n_nodes * a.C + ch, h);
+}
+
 // ---------------------------------------------------------------------------------------------
 // host side
 
@@ -1459,27 +1574,42 @@ int scan_map(CUtensorMap* m, const void* base, int C, int N) {
   return sizeof(T) == 2 ? make_tmap_bf16_2d(m, base, C, N, box, kTile) : make_tmap_f32_2d(m, base, C, N, box, kTile);
 }
 
-// A block an SM, or one for each unit of work.  The kernel's shared memory is announced once a device.
+// The SMs of the current device; the kernel's dynamic shared memory is announced there, once a device.
 template <auto KERN, int SMEM>
-int scan_grid(int64_t units, unsigned* blocks) {
+int announce(int* sms = nullptr) {
   static std::atomic<int> sms_of[64];              // one array a kernel; 0: not announced yet
-  int dev = 0, sms = 0;
+  int dev = 0, n = 0;
   int rc = record_cuda(cudaGetDevice(&dev));
   if (rc) return rc;
-  if (dev < 64) sms = sms_of[dev].load(std::memory_order_acquire);
-  if (!sms) {
+  if (dev < 64) n = sms_of[dev].load(std::memory_order_acquire);
+  if (!n) {
     rc = record_cuda(cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
-    if (!rc) rc = record_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
+    if (!rc) rc = record_cuda(cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev));
     if (rc) return rc;
-    if (dev < 64) sms_of[dev].store(sms, std::memory_order_release);
+    if (dev < 64) sms_of[dev].store(n, std::memory_order_release);
   }
-  *blocks = (unsigned)std::min<int64_t>(units, sms);
+  if (sms) *sms = n;
   return TREE_OK;
+}
+// a block an SM, or one for each unit of work
+template <auto KERN, int SMEM>
+int scan_grid(int64_t units, unsigned* blocks) {
+  int sms = 0;
+  const int rc = announce<KERN, SMEM>(&sms);
+  if (!rc) *blocks = (unsigned)std::min<int64_t>(units, sms);
+  return rc;
 }
 
 // 12 bytes a channel are marked empty for each tile: a block for 1024 channels
 dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (unsigned)((C + 1023) / 1024)); }
 
+template <typename T, int KIND>
+int run_step(const ScanFwd<T>& a, const void* gate, const void* x, cudaStream_t s) {
+  int rc = announce<&k_scan_step<T, KIND>, step_smem<T>(kTile)>();
+  if (rc) return rc;
+  k_scan_step<T, KIND><<<a.slabs, 32 * kStepWarps, step_smem<T>(a.t.N), s>>>(static_cast<const T*>(gate), static_cast<const T*>(x), a);
+  return record_cuda(cudaGetLastError());
+}
 template <typename T, int KIND>
 int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, cudaStream_t s) {
   unsigned blocks = 0;
@@ -1501,12 +1631,15 @@ template <typename T>
 int scan_fwd(const ScanTree& t, const ScanWork& w, const void* gate, const void* x, const float* init, int C, int dtype,
              int kind, void* y, float* states, int32_t* status, cudaStream_t s) {
   const int slabs = scan_slabs(C, dtype);
+  const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
+  if (t.N <= kTile)
+    return kind == TREE_GATE_SIGMOID ? run_step<T, TREE_GATE_SIGMOID>(a, gate, x, s)
+                                     : run_step<T, TREE_GATE_LOG>(a, gate, x, s);
   CUtensorMap tg, tx;
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (rc) return rc;
   k_scan_prepare<<<prepare_grid(t, C), kTile, 0, s>>>(t, w, slabs, C, 0, states, states + (size_t)t.n_nodes * C);
-  const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_fwd<T, TREE_GATE_SIGMOID>(a, tg, tx, s)
                                    : run_fwd<T, TREE_GATE_LOG>(a, tg, tx, s);
 }
