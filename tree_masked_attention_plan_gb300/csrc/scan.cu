@@ -35,7 +35,7 @@ namespace {
 
 constexpr int kTile = TREE_SCAN_TILE;       // tokens of a tile
 constexpr int kScanWarps = 8;               // warps that share a tile: 8 tokens each
-constexpr int kFwdSlots = kTile == 64 ? 6 : 3, kBwdSlots = kTile == 64 ? 5 : 3, kPlanes = 4;     // 160 to 192 KB: a block an SM
+constexpr int kSlots = 3, kPlanes = 4;       // tiles that a block holds, 64 KB each: a block an SM
 // a block: mapping warps (eight times kFwdMaps, on one tile), groups of eight walking warps, one warp that loads, one
 // that publishes, some that join; groups and joining warps take tiles in turn
 constexpr int kFwdMaps = 2, kFwdWalks = 1, kFwdJoins = 3, kBwdMaps = 1, kBwdWalks = 1, kBwdJoins = 2;
@@ -472,8 +472,8 @@ struct ScanShared {
   alignas(16) float all[SLOTS][2][64];             // the tile's map
   alignas(16) float in[SLOTS][64];                 // the state before (the gradient behind) the tile
 };
-using FwdShared = ScanShared<kFwdSlots, kFwdMaps>;
-using BwdShared = ScanShared<kBwdSlots, kBwdMaps>;
+using FwdShared = ScanShared<kSlots, kFwdMaps>;
+using BwdShared = ScanShared<kSlots, kBwdMaps>;
 // A group of walking warps among themselves.
 struct ScanWalk {
   uint64_t own, turn[kScanWarps];                  // all of them are here; carry of the warp before is there
@@ -483,7 +483,7 @@ struct ScanWalk {
   int row_of[kTile];
 };
 struct ScanBack {
-  alignas(16) float R[kBwdSlots][kScanWarps][64];      // the gradient's map is u -> A u + R
+  alignas(16) float R[kSlots][kScanWarps][64];      // the gradient's map is u -> A u + R
   alignas(16) float before[kScanWarps][kWarpTokens / 4][64];     // h before every fourth token, where it cannot stay in registers
 };
 
@@ -1135,20 +1135,25 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
       f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
       f.joins = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
     }
-    const bool slow = f.breaks | f.joins;
+    const uint32_t special = f.breaks | f.joins;
+    // the four tokens in which the warp's first break lies: up to there h depends on what comes into the warp
+    const int known = f.breaks ? (__ffs(f.breaks) - 1) & ~3 : kWarpTokens - 4;
     const bool near = __any_sync(0xffffffffu, f.kid_at >= 0);         // a node of this tile joins in the warp
     if (!wait_phase(mapped ? &sh.known[t.s] : &sh.mapped[t.s], t.parity, wc)) return;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
         Vec<CH> v = vec<CH>(0.f), b[4];
 #pragma unroll 1
-        for (int g = 0; g < kWarpTokens; g += 4) f.befores(g, v, b);
+        for (int g = known; g < kWarpTokens; g += 4) {
+          sh_st(back.before[warp][g / 4], v);
+          f.befores(g, v, b);
+        }
         sh_st(sh.B[t.s][warp], v);
       }
-      if (slow && !near) {
+      if (special && !near) {                          // what the warp hands on depends on its tokens up to there
         Vec<CH> R = vec<CH>(0.f), d[4];
 #pragma unroll 1
-        for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
+        for (int g = known; g >= 0; g -= 4) {
           f.sums(g, d);
 #pragma unroll
           for (int q = 3; q >= 0; --q) {
@@ -1173,21 +1178,13 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
     }
     // h before every fourth token; the others are stepped to again on the way back (16 values a lane would stay in
     // registers only in straight-line code of 15 KB, which the warps' other code would push out of the cache)
-    if (!slow) {
-#pragma unroll 4
-      for (int q = 0; q < kWarpTokens - 4; ++q) {
-        if (q % 4 == 0) sh_st(back.before[warp][q / 4], h);
-        h = advance<KIND>(rows.p(q), rows.get(1, q), h);
-      }
-      sh_st(back.before[warp][kWarpTokens / 4 - 1], h);
-    } else {
-      Vec<CH> b[4];
 #pragma unroll 1
-      for (int g = 0; g < kWarpTokens; g += 4) {
-        sh_st(back.before[warp][g / 4], h);
-        f.befores(g, h, b);
-      }
+    for (int g = 0; g < known; g += 4) {
+      sh_st(back.before[warp][g / 4], h);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) h = advance<KIND>(rows.p(g + q), rows.get(1, g + q), h);
     }
+    sh_st(back.before[warp][known / 4], h);
     // the gradient behind the warp, as the state before it in the forward
     auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles before
       if (serial && warp > 0) {
@@ -1221,16 +1218,20 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
     // token q: lam = what reaches it; its gradients; u before it
     auto step = [&](int q, Vec<CH> lam, Vec<CH> before) {
       const Vec<CH> p = rows.p(q);
-      u = decayed(p, lam);
       Vec<CH> dx, dg;
       if (KIND == TREE_GATE_SIGMOID) {
-        Vec<CH> m;                                     // the smaller of a and 1 - a, and the larger
+        Vec<CH> m, n;                                  // the smaller of a and 1 - a: m; lam by it, and by the larger
 #pragma unroll
-        for (int c = 0; c < CH; ++c) m.v[c] = fabsf(p.v[c]);
-        const Vec<CH> l = vec<CH>(1.f) - m;
-        dx = lam * pick(p, m, l);
-        dg = lam * (m * l) * (before - rows.get(1, q));
+        for (int c = 0; c < CH; ++c) {
+          m.v[c] = fabsf(p.v[c]);
+          n.v[c] = -m.v[c];
+        }
+        const Vec<CH> v = m * lam, w = vfma(n, lam, lam);
+        u = pick(p, w, v);
+        dx = pick(p, v, w);
+        dg = vfma(n, v, v) * (before - rows.get(1, q));
       } else {
+        u = decayed(p, lam);
         dx = lam;
         dg = u * before;
 #pragma unroll
@@ -1242,7 +1243,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
         *reinterpret_cast<uint32_t*>(a.dx + at) = Lane<T>::pack(dx);
       }
     };
-    if (!slow) {
+    if (!special) {
 #pragma unroll 1
       for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
         Vec<CH> b[4];
@@ -1252,11 +1253,20 @@ DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk&
 #pragma unroll
         for (int q = 3; q >= 0; --q) step(g + q, rows.get(2, g + q) + u, b[q]);
       }
-    } else {
+    } else
 #pragma unroll 1
-      for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
-        Vec<CH> b[4], d[4], hg = sh_ld<CH>(back.before[warp][g / 4]);
-        f.befores(g, hg, b);
+    for (int g = kWarpTokens - 4; g >= 0; g -= 4) {
+      Vec<CH> b[4];
+      h = sh_ld<CH>(back.before[warp][g / 4]);
+      if (!((special >> g) & 15u)) {
+        b[0] = h;
+#pragma unroll
+        for (int q = 0; q < 3; ++q) b[q + 1] = advance<KIND>(rows.p(g + q), rows.get(1, g + q), b[q]);
+#pragma unroll
+        for (int q = 3; q >= 0; --q) step(g + q, rows.get(2, g + q) + u, b[q]);
+      } else {
+        Vec<CH> d[4];
+        f.befores(g, h, b);
         for (uint32_t m = near ? (f.joins >> g) & 15u : 0u; m; m &= m - 1) {
           const int at = __shfl_sync(0xffffffffu, f.kid_at, g + __ffs(m) - 1);
           if (at >= 0 && (at - warp * kWarpTokens) / 4 != g / 4) wait_row(at);      // (those of these four: below)
@@ -1504,7 +1514,8 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
     }
     if (w > warp && rt) return;
   }
-  if (on && N == kTile) st_state(a.states + (size_t)a.t.n_nodes * a.C + ch, h);
+  // the row behind the tile, which nothing here goes on from, holds no leftovers
+  if (on) st_state(a.states + (size_t)a.t.n_nodes * a.C + ch, N == kTile ? h : vec<CH>(0.f));
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1613,17 +1624,17 @@ int run_step(const ScanFwd<T>& a, const void* gate, const void* x, cudaStream_t 
 template <typename T, int KIND>
 int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, cudaStream_t s) {
   unsigned blocks = 0;
-  const int rc = scan_grid<&k_scan_fwd<T, KIND>, scan_smem(kFwdSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_fwd<T, KIND>, scan_smem(kSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), scan_smem(kFwdSlots), s>>>(tg, tx, a);
+  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), scan_smem(kSlots), s>>>(tg, tx, a);
   return record_cuda(cudaGetLastError());
 }
 template <typename T, int KIND>
 int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, const CUtensorMap& td, cudaStream_t s) {
   unsigned blocks = 0;
-  const int rc = scan_grid<&k_scan_bwd<T, KIND>, scan_smem(kBwdSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
+  const int rc = scan_grid<&k_scan_bwd<T, KIND>, scan_smem(kSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), scan_smem(kBwdSlots), s>>>(tg, tx, td, a);
+  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), scan_smem(kSlots), s>>>(tg, tx, td, a);
   return record_cuda(cudaGetLastError());
 }
 
