@@ -385,8 +385,9 @@ size_t tree_scan_workspace(const tree_plan_t* plan, int C);
  * gate, x, y: [N][C] in packed order, all of type dtype (TREE_BF16 or TREE_F32).
  * states: fp32 [tree_scan_rows()][C].  Row v < n_nodes receives node v's final state (zeros where the
  * node holds no tokens); the rows behind them are for the backward (row n_nodes + k: the state after
- * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout; y is rounded once.  A state that becomes
- * infinite or NaN stays so (either) along its paths and touches no other path.
+ * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout; y is rounded
+ * once.  A state that becomes infinite or NaN stays so (either) along its paths and touches no
+ * other path.
  * C a multiple of 8 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
  * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at
  * a time.  Deterministic.  status_dev (device int32, may be NULL) as for tree_attn_fwd. */
@@ -454,8 +455,8 @@ typedef struct {
 size_t tree_grad_workspace(int n);
 
 /* *norm (device fp32) = sqrt of the sum of squares of every element of the n >= 1 gradients (the
- * list is host memory, free when the call returns).  Summed in fp64; the norm is right wherever it
- * is an fp32 number, also where the squares are not.  Infinite or NaN elements give such a norm.
+ * list is host memory, free when the call returns).  The sum is held in pairs of fp32 and in fp64; the
+ * norm is right wherever it is an fp32 number, also where the squares are not.  Infinite or NaN elements give such a norm.
  * Deterministic. */
 int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
                    tree_stream_t stream);

@@ -1,10 +1,14 @@
 """The gated linear recurrence against its fp64 oracle, forward and backward.
 
 Tolerances: the oracle carries, next to every value, how many fp32 roundings of what magnitude reach it
-(one unit a token).  A token costs: the gate's p and the input b (exp 2 ulp, reciprocal, two products: 9
-half ulps of 2^-24), the step itself (2), the same again where the sequence is cut into tiles whose
-products and sums are joined (11): 24 units of 2^-24 cover it.  Results in bf16 add half a step, 2^-8 of
-the value; fp32 results 2^-24."""
+(one unit a token, counted in units of 2^-24).  A token costs, forward: e = exp(-g) as 2^t, t = -g log2(e):
+the constant (0.3 |g|) and the product (half a unit in the last place of t, 5.5 for |g| <= 11 after the
+factor ln 2) and the power (2 ulp: 4); 1 - a = e a adds the reciprocal (2) and a product (1), less where e is
+large, and e's own part of it is e's weight 1 / (1 + e) there and e / (1 + e) in a: together at most 15 of the
+larger of the two; times x 1, the step 1, and where the sequence is cut into tiles their products and sums
+(2 per joined map, 4 a tile of 128: below 1).  Backward: p's exponential carries what its argument lost
+(2 ulp and 1), a reciprocal and a product (3), the step 2, once more for h, which is computed again: 16.  24
+units cover both.  Results in bf16 add half a step, 2^-8 of the value; fp32 results 2^-24."""
 import numpy as np
 import pytest
 import torch
@@ -246,3 +250,109 @@ def test_guards_around_every_buffer():
         assert bool((raw[:4096] == 0xA5).all()) and bool((raw[4096 + b:] == 0xA5).all())
     for t in (st, di):
         assert torch.isfinite(t).all() and t.abs().max() < 1e3
+
+
+@pytest.mark.parametrize("kind,dtype", [("sigmoid", torch.bfloat16), ("log", torch.float32)])
+@pytest.mark.parametrize("seed,n_nodes,max_len,zero,C", [(0, 5, 40, 0, 8), (1, 20, 6, 0.2, 72), (2, 60, 2, 0.3, 136),
+                                                         (3, 128, 1, 0, 40), (4, 700, 1, 0.9, 64)])
+def test_few_tokens(kind, dtype, seed, n_nodes, max_len, zero, C):
+    """At most 128 tokens: chains, paths that part within a few tokens, many trees, many nodes without tokens."""
+    parent, node_len = random_tree(450 + seed, n_nodes, max_len=max_len, zero_prob=zero, n_roots=1 + 3 * seed)
+    assert 1 <= node_len.sum() <= 128
+    check(parent, node_len, C, kind, dtype, seed, ends=seed % 2 == 1)
+
+
+def test_few_and_many_tokens_agree():
+    """A sequence of 128 tokens and the first 128 of a longer one; the states row between tiles is the state there."""
+    C = 64
+    gate, x, _, _, _ = _inputs(300, 1, C, "sigmoid", torch.float32, 14)
+    d = lambda t: t.to(DEV)
+    res = []
+    for n in (128, 300):
+        plan, tree = tam.tree_plan([-1], [n], device=DEV), tam.tree_arrays([-1], [n], DEV)
+        res.append(tam.tree_scan_fwd(plan, tree, d(gate[:n].contiguous()), d(x[:n].contiguous())))
+    ref = osc.scan([-1], [128], _f64(gate[:128]), _f64(x[:128]), "sigmoid")
+    for y, _ in res:
+        _close("y", y[:128], ref["y"], ref["e_y"], torch.float32)
+    assert torch.equal(res[0][1][1], res[0][1][0]) and torch.equal(res[0][1][0], res[0][0][127])
+    _close("between", res[1][1][1:2], ref["y"][127:], ref["e_y"][127:], torch.float32)
+
+
+def test_many_calls_of_a_tree_of_short_nodes():
+    """Many slabs of tiles full of breaks, again and again: every wait ends and no bit changes."""
+    parent, node_len = random_tree(460, 300, max_len=30, zero_prob=0.1, n_roots=9)
+    N, n, C = int(node_len.sum()), 300, 1000
+    gate, x, init, dy, dfin = (t.to(DEV) for t in _inputs(N, n, C, "log", torch.float32, 15))
+    plan, tree = tam.tree_plan(parent, node_len, device=DEV), tam.tree_arrays(parent, node_len, DEV)
+    ws = torch.empty(tam.tree_scan_workspace(plan, C), dtype=torch.uint8, device=DEV)
+    status = tam.new_status(DEV)
+    first = None
+    for i in range(60):
+        y, st = tam.tree_scan_fwd(plan, tree, gate, x, init=init, gate_kind="log", workspace=ws, status=status)
+        now = (y, st) + tam.tree_scan_bwd(plan, tree, gate, x, st, dy, init=init, d_final=dfin, gate_kind="log",
+                                          workspace=ws, status=status)
+        first = first or now
+        if i % 20 == 19:
+            assert all(torch.equal(a, b) for a, b in zip(first, now))
+    torch.cuda.synchronize()
+    tam.check_status(status, "scan")
+
+
+def test_two_streams_at_once_and_two_graphs_of_one_workspace():
+    parent, node_len = random_tree(470, 60, max_len=150, n_roots=2)
+    N, n, C = int(node_len.sum()), 60, 2056
+    plan, tree = tam.tree_plan(parent, node_len, device=DEV), tam.tree_arrays(parent, node_len, DEV)
+    ins = [[t.to(DEV) for t in _inputs(N, n, C, "sigmoid", torch.bfloat16, 16 + i)] for i in range(2)]
+    status = tam.new_status(DEV)
+
+    def call(i, ws, stream=None):
+        gate, x, init, dy, dfin = ins[i]
+        y, st = tam.tree_scan_fwd(plan, tree, gate, x, init=init, workspace=ws, status=status, stream=stream)
+        return (y, st) + tam.tree_scan_bwd(plan, tree, gate, x, st, dy, init=init, d_final=dfin, workspace=ws,
+                                           status=status, stream=stream)
+
+    own = [torch.empty(tam.tree_scan_workspace(plan, C), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    alone = [call(i, own[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream(DEV) for _ in range(2)]
+    both = [[call(i, own[i], side[i]) for i in range(2)] for _ in range(4)]      # blocks of both calls share the GPU
+    torch.cuda.synchronize()
+    for pair in both:
+        for i in range(2):
+            assert all(torch.equal(a, b) for a, b in zip(alone[i], pair[i]))
+    graphs, got = [torch.cuda.CUDAGraph() for _ in range(2)], [None, None]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            got[i] = call(i, own[0])
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(alone[i], got[i]))
+    tam.check_status(status, "scan")
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 elements: the last channels of a sequence whose every tensor is 8.6 GB."""
+    N, C = 131072, 32776
+    free, _ = torch.cuda.mem_get_info(DEV)
+    if free < 100e9:
+        pytest.skip("needs 100 GB of device memory")
+    plan, tree = tam.tree_plan([-1], [N], device=DEV), tam.tree_arrays([-1], [N], DEV)
+    ch = np.r_[0:2, C - 4:C]
+    # the same six channels' values everywhere but at the sampled ones, which are their own
+    gate, x, _, dy, _ = _inputs(N, 1, len(ch), "sigmoid", torch.bfloat16, 17)
+
+    def wide(t):
+        w = torch.zeros(N, C, dtype=t.dtype, device=DEV)
+        w[:, torch.as_tensor(ch, device=DEV)] = t.to(DEV)
+        return w
+
+    g, v, d = wide(gate), wide(x), wide(dy)
+    y, st = tam.tree_scan_fwd(plan, tree, g, v)
+    dg, dx, _ = tam.tree_scan_bwd(plan, tree, g, v, st, d)
+    ref = osc.scan([-1], [N], _f64(gate), _f64(x), "sigmoid", dy=_f64(dy))
+    idx = torch.as_tensor(ch, device=DEV)
+    for name, got in (("y", y), ("dgate", dg), ("dx", dx)):
+        _close(name, got[:, idx], ref[name], ref["e_" + name], torch.bfloat16)
+    _close("final", st[:1, idx], ref["final"], ref["e_final"], torch.float32)

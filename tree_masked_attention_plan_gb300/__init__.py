@@ -671,7 +671,7 @@ def tree_scan_workspace(plan: TreePlan, C) -> int:
 
 
 def tree_scan_rows(plan: TreePlan) -> int:
-    """Rows of tree_scan_fwd's states: the nodes', then one for every 64 tokens."""
+    """Rows of tree_scan_fwd's states: the nodes', then one for every TREE_SCAN_TILE (128) tokens."""
     return int(_lib().tree_scan_rows(plan.ref()))
 
 

@@ -7,7 +7,8 @@
 // turn, so that pos * frequency wraps modulo one turn by itself in integer arithmetic, and only
 // the wrapped fraction becomes a float (error 2^-25 turns, where pos * frequency in fp32 loses
 // whole radians beyond position 10^6).
-// HBM-bound: every head of q and k is read and written once.
+// HBM-bound: every head of q and k is read and written once.  32768 tokens of 40 heads of 128: 104 us, 6.4 TB/s;
+// the gradient of 9973 tokens of 32 heads of 64: 16.5 us, 5.0 TB/s (82 MB, of which much stays in L2).
 #include <cmath>
 
 #include "common.cuh"
@@ -118,7 +119,7 @@ int rope_axes(const tree_plan_t* plan, const int32_t* pos, const int32_t* sectio
   const int N = plan->n_tokens;
   const int rows = d == 128 ? 4 : 8;
   // One warp a token once there are enough of them to fill the GPU; with few tokens a token's
-  // heads are dealt to several warps (48 tokens of 40 heads: ten warps each).
+  // heads are dealt to several warps (48 tokens of 40 heads: ten warps each, 2.6 us instead of 5.5).
   const int most = (Hq + Hkv + rows - 1) / rows;
   int split = 1;
   while (split < most && (int64_t)N * split < 152 * 16) ++split;

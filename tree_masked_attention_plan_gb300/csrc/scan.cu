@@ -10,7 +10,7 @@
 // final state of a node that lies before it.
 //
 // HBM-bound: the forward reads g and x and writes y once, the backward reads g, x, dy and writes
-// dg, dx once.  A unit of work is a tile of 64 tokens by 128 bytes of channels.  A step of the
+// dg, dx once.  A unit of work is a tile of 128 tokens by 128 bytes of channels.  A step of the
 // recurrence is the map h -> a h + b, and maps compose, so a tile needs its neighbours for one
 // value per channel only: it adds its own 128 steps up to one map, publishes that, takes the state
 // before it from the maps of the tiles before it, and then knows every h.  Tiles are handed out
@@ -19,10 +19,18 @@
 // The order in which states and maps are joined depends on the tree alone: the result does not
 // change from run to run.
 //
-// Precision: states, gates and gradients are fp32.  A decay close to one is held as what it
-// lacks to one: p = -(1 - a) where a > 1/2, p = a elsewhere, so that a memory of thousands of
-// tokens does not lose its length to the rounding of a; the step h + (p h + b) then adds a small
-// increment to h.
+// Measured (bf16, 268M elements, sigmoid gate): one sequence of 32768 tokens by 8192 channels forward
+// 0.34 ms, 4.7 TB/s, backward 0.61 ms, 4.4 TB/s; a tree of the same size (nodes of some 250 tokens) 0.41 and
+// 0.77 ms.  What bounds it there is instruction issue and the dependent steps of a warp's walk (in the backward a
+// step of 64 channels takes 120 instructions, and the SM issues in 57 % of all cycles; the copies alone, without
+// the arithmetic, take 0.27 ms in the forward).  In a tree of short nodes it is the way of a state through the
+// tiles, one after the other: 3456 tokens of a caterpillar by 4096 channels take 103 us, 13 at the memory's rate.
+// Why 128 tokens: a tile hands on 4 bytes of state and 8 of map for each channel, and one of 64 tokens twice as
+// often (the tree: 0.53 instead of 0.42 ms forward, 1.00 instead of 0.78 backward).
+//
+// Precision: states, gates and gradients are fp32.  The forward holds a and 1 - a apart, each with the accuracy
+// of its own size.  The backward has one word for both: p = -(1 - a) where a > 1/2, p = a elsewhere, so
+// that neither the little that a long memory loses a token nor a small decay drowns in the other's rounding.
 #include <algorithm>
 #include <atomic>
 
@@ -34,16 +42,17 @@ int make_tmap_bf16_2d(CUtensorMap* m, const void* base, int inner, int rows, int
 namespace {
 
 constexpr int kTile = TREE_SCAN_TILE;       // tokens of a tile
-constexpr int kScanWarps = 8;               // warps that share a tile: 8 tokens each
+constexpr int kScanWarps = 8;               // warps that share a tile: 16 tokens each
 constexpr int kSlots = 3, kPlanes = 4;       // tiles that a block holds, 64 KB each: a block an SM
-// a block: mapping warps (eight times kFwdMaps, on one tile), groups of eight walking warps, one warp that loads, one
-// that publishes, some that join; groups and joining warps take tiles in turn
-constexpr int kFwdMaps = 2, kFwdWalks = 1, kFwdJoins = 3, kBwdMaps = 1, kBwdWalks = 1, kBwdJoins = 2;
-constexpr int scan_threads(int maps, int walks, int joins) { return 32 * ((maps + walks) * kScanWarps + 2 + joins); }
+// A block: eight mapping warps, eight walking warps, one warp that loads, one that publishes, two that join, which take
+// tiles in turn (three cost the backward a tenth).  Sixteen mapping warps in the forward: one sequence of 32768 x 8192
+// in 0.33 ms instead of 0.34, but trees (which the walking warps bound) slower, the caterpillar 115 us instead of 103.
+// A second group of walking warps in the backward leaves 72 registers a thread, which spill: the rollout 0.95 -> 1.72 ms.
+constexpr int kJoins = 2, kScanThreads = 32 * (2 * kScanWarps + 2 + kJoins);
 constexpr int kWarpTokens = kTile / kScanWarps;
 constexpr int kRow = 128;                   // bytes of a tile's row: 64 bf16 or 32 fp32 channels, a word a lane
 constexpr int kPlane = kTile * kRow;         // one tensor's rows of a tile
-constexpr int kScanGroup = 8;               // at most this many maps are joined to a state
+constexpr int kScanGroup = 4;               // at most this many maps are joined to a state (8: 131072 x 2048 2 % slower)
 
 constexpr int kLinkChain = -1;             // the token before on the path is the one before in packed order
 constexpr int kLinkRoot = -2;              // the token starts from its node's initial state
@@ -450,7 +459,7 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
       : "memory");
 }
 
-// A block works on up to SLOTS tiles at a time, in the order in which it drew them:
+// A block works on up to kSlots tiles at a time, in the order in which it drew them:
 //   loading warp      draws a tile, starts its copies                                       -> drawn, full
 //   joining warp      looks up what the tile holds                                          -> told
 //   mapping warps     the map of every token (backward: its p) and of every warp's tokens    -> mapped
@@ -459,22 +468,19 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
 //   walking warps     wait for that state, write the results                                 -> empty
 // So a tile whose state is late holds up nothing that another tile waits for: its map is out, and so are
 // those of the tiles that the block drew after it.
-template <int SLOTS, int MAPS>
 struct ScanShared {
-  uint64_t drawn[SLOTS], full[SLOTS], told[SLOTS], mapped[SLOTS], known[SLOTS], ready[SLOTS], empty[SLOTS];
-  int tile[SLOTS], slab[SLOTS], info[SLOTS];
+  uint64_t drawn[kSlots], full[kSlots], told[kSlots], mapped[kSlots], known[kSlots], ready[kSlots], empty[kSlots];
+  int tile[kSlots], slab[kSlots], info[kSlots];
   int abort_flag;
-  int reset[SLOTS][kScanWarps];
+  int reset[kSlots][kScanWarps];
   // Per warp and channel the map of its tokens; in a tile without breaks the publishing warp puts that of all
   // tokens before the warp there (backward: in B the state before it, in A and R the gradient's map behind it).
-  alignas(16) float A[SLOTS][kScanWarps * MAPS][64];
-  alignas(16) float B[SLOTS][kScanWarps * MAPS][64];
-  alignas(16) float all[SLOTS][2][64];             // the tile's map
-  alignas(16) float in[SLOTS][64];                 // the state before (the gradient behind) the tile
+  alignas(16) float A[kSlots][kScanWarps][64];
+  alignas(16) float B[kSlots][kScanWarps][64];
+  alignas(16) float all[kSlots][2][64];             // the tile's map
+  alignas(16) float in[kSlots][64];                 // the state before (the gradient behind) the tile
 };
-using FwdShared = ScanShared<kSlots, kFwdMaps>;
-using BwdShared = ScanShared<kSlots, kBwdMaps>;
-// A group of walking warps among themselves.
+// The walking warps among themselves.
 struct ScanWalk {
   uint64_t own, turn[kScanWarps];                  // all of them are here; carry of the warp before is there
   alignas(16) float carry[kScanWarps][64];         // the state before (gradient behind) a warp, where they go one by one
@@ -501,7 +507,6 @@ struct ScanEnds {
   alignas(16) float state[kTile / kKeep][64];
 };
 
-
 template <typename T>
 struct ScanFwd {
   const float* init;
@@ -527,16 +532,16 @@ struct ScanBwd {
 };
 
 // The loading warp: draws tiles from the counter and starts their copies.
-template <bool FWD, int SLOTS, int MAPS, int TENSORS>
-DEVI void scan_load(ScanShared<SLOTS, MAPS>& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
+template <bool FWD, int TENSORS>
+DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
                     int tiles, int slabs, int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   auto draw = [&] { return atomicAdd(reinterpret_cast<unsigned long long*>(w.ctl), 1ull); };
   unsigned long long next = lane == 0 ? draw() : 0;
   int i = 0, ends = 0;
   for (;; ++i) {
-    const int s = i % SLOTS;
-    if (i >= SLOTS && !wait_phase(&sh.empty[s], ((i / SLOTS) - 1) & 1, wc)) break;
+    const int s = i % kSlots;
+    if (i >= kSlots && !wait_phase(&sh.empty[s], ((i / kSlots) - 1) & 1, wc)) break;
     const unsigned long long ticket = __shfl_sync(0xffffffffu, next, 0);
     // tile by tile, its slabs side by side
     const unsigned long long turn = ticket >> 32 ? ticket / (unsigned)slabs : (uint32_t)ticket / (uint32_t)slabs;
@@ -547,7 +552,7 @@ DEVI void scan_load(ScanShared<SLOTS, MAPS>& sh, uint8_t* slots, const CUtensorM
         mbar_arrive(&sh.told[s]);
         mbar_arrive(&sh.full[s]);
       }
-      if (++ends == SLOTS) break;
+      if (++ends == kSlots) break;
       continue;
     }
     const int slab = static_cast<int>(ticket - turn * (unsigned)slabs);
@@ -562,7 +567,7 @@ DEVI void scan_load(ScanShared<SLOTS, MAPS>& sh, uint8_t* slots, const CUtensorM
         tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * kTile);
     }
     // The first tiles are drawn one at a time, so that neighbours go to different blocks; later ones ahead.
-    if (i + 1 < SLOTS && !wait_phase(&sh.full[s], 0, wc)) {
+    if (i + 1 < kSlots && !wait_phase(&sh.full[s], 0, wc)) {
       ++i;
       break;
     }
@@ -571,9 +576,9 @@ DEVI void scan_load(ScanShared<SLOTS, MAPS>& sh, uint8_t* slots, const CUtensorM
   // every copy has landed before the block's shared memory goes, also where other warps gave up
   // (slots that hold an end had their copies used before)
   if (lane == 0)
-    for (int q = max(0, i - SLOTS); q < i; ++q) {
+    for (int q = max(0, i - kSlots); q < i; ++q) {
       const uint64_t t0 = global_timer_ns();
-      while (sh.tile[q % SLOTS] >= 0 && !mbar_try_wait(&sh.full[q % SLOTS], (q / SLOTS) & 1) &&
+      while (sh.tile[q % kSlots] >= 0 && !mbar_try_wait(&sh.full[q % kSlots], (q / kSlots) & 1) &&
              global_timer_ns() - t0 < wc.limit_ns) {
       }
     }
@@ -585,10 +590,9 @@ struct Tile {
   uint32_t parity;
 };
 // `bar`: what of the tile is waited for; a tile number of -1 there is the end
-template <int SLOTS, int MAPS>
-DEVI bool next_tile(ScanShared<SLOTS, MAPS>& sh, uint64_t (&bar)[SLOTS], int i, Tile& t, const WaitCtl& wc) {
-  t.s = i % SLOTS;
-  t.parity = (i / SLOTS) & 1;
+DEVI bool next_tile(const ScanShared& sh, uint64_t (&bar)[kSlots], int i, Tile& t, const WaitCtl& wc) {
+  t.s = i % kSlots;
+  t.parity = (i / kSlots) & 1;
   if (!wait_phase(&bar[t.s], t.parity, wc)) return false;
   t.k = sh.tile[t.s];
   t.slab = sh.slab[t.s];
@@ -607,8 +611,8 @@ template <typename T>
 struct Rows {
   uint8_t *base, *pair;
   static constexpr int CH = Lane<T>::CH;
-  DEVI Rows(uint8_t* slots, int s, int warp, int first = 0) {
-    const int lane = threadIdx.x & 31, row = warp * kWarpTokens + first;
+  DEVI Rows(uint8_t* slots, int s, int warp) {
+    const int lane = threadIdx.x & 31, row = warp * kWarpTokens;
     base = slots + (size_t)s * kPlanes * kPlane + row * kRow + lane * 4;
     pair = slots + ((size_t)s * kPlanes + 2) * kPlane + row * 2 * kRow + lane * 8;
   }
@@ -686,7 +690,7 @@ struct Joiner {
 
 // The publishing warp.  It waits for no other block, so that a tile's map is out as soon as it can be.
 template <int CH>
-DEVI void fwd_publish(FwdShared& sh, const ScanWork& w, int C, int slab_ch, const WaitCtl& wc) {
+DEVI void fwd_publish(ScanShared& sh, const ScanWork& w, int C, int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
   for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
@@ -694,12 +698,10 @@ DEVI void fwd_publish(FwdShared& sh, const ScanWork& w, int C, int slab_ch, cons
     if (t.info & kInfoMapped) {
       Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
 #pragma unroll 8
-      for (int q = 0; q < kScanWarps * kFwdMaps; ++q) {
+      for (int q = 0; q < kScanWarps; ++q) {
         const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]), qb = sh_ld<CH>(sh.B[t.s][q]);
-        if (q % kFwdMaps == 0) {
-          sh_st(sh.A[t.s][q], A);
-          sh_st(sh.B[t.s][q], B);
-        }
+        sh_st(sh.A[t.s][q], A);
+        sh_st(sh.B[t.s][q], B);
         B = vfma(qa, B, qb);
         A = A * qa;
       }
@@ -714,7 +716,7 @@ DEVI void fwd_publish(FwdShared& sh, const ScanWork& w, int C, int slab_ch, cons
 
 // after: the states between tiles, which the forward left
 template <int CH>
-DEVI void bwd_publish(BwdShared& sh, ScanBack& back, const ScanWork& w, const float* after, int C,
+DEVI void bwd_publish(ScanShared& sh, ScanBack& back, const ScanWork& w, const float* after, int C,
                       int slab_ch, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
@@ -750,12 +752,12 @@ DEVI void bwd_publish(BwdShared& sh, ScanBack& back, const ScanWork& w, const fl
 // state behind the nearest tile before it that is no plain map or ends a group of kScanGroup; backward the same
 // from the other side.  Groups bound the maps that a tile joins; within one, no tile waits for a state to be
 // handed on.  rows: the states between tiles (backward: the gradients).
-template <bool FWD, int CH, int JOINS, int SLOTS, int MAPS>
-DEVI void scan_join(ScanShared<SLOTS, MAPS>& sh, const ScanWork& w, int C, int tiles, float* rows, int slab_ch, bool joins,
+template <bool FWD, int CH>
+DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, int tiles, float* rows, int slab_ch, bool joins,
                     int joiner, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
-  for (int i = joiner; next_tile(sh, sh.drawn, i, t, wc); i += JOINS) {
+  for (int i = joiner; next_tile(sh, sh.drawn, i, t, wc); i += kJoins) {
     const int n = FWD ? t.k - lane : t.k + lane;
     int info = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
     // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
@@ -783,17 +785,16 @@ DEVI void scan_join(ScanShared<SLOTS, MAPS>& sh, const ScanWork& w, int C, int t
   }
 }
 
-// The mapping warps, forward, all on one tile: a and b of every token, and the map of kMapTokens of them.
-constexpr int kMapTokens = kWarpTokens / kFwdMaps;
+// The mapping warps, forward: a and b of every token, and the map of a warp's tokens.
 template <typename T, int KIND>
-DEVI void fwd_map(FwdShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
+DEVI void fwd_map(ScanShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH;
   Tile t;
   for (int i = 0; next_tile(sh, sh.full, i, t, wc); ++i) {
-    const Rows<T> rows(slots, t.s, warp / kFwdMaps, warp % kFwdMaps * kMapTokens);
+    const Rows<T> rows(slots, t.s, warp);
     Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
 #pragma unroll 4
-    for (int q = 0; q < kMapTokens; ++q) {
+    for (int q = 0; q < kWarpTokens; ++q) {
       Vec<CH> a, b;
       token_of<KIND>(rows.get(0, q), rows.get(1, q), a, b);
       rows.set_token(q, a, b);
@@ -807,7 +808,7 @@ DEVI void fwd_map(FwdShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
   }
 }
 
-// Forward, the runs of a warp's 8 tokens between breaks and what is to be kept of them.  Loops are rolled: this
+// Forward, the runs of a warp's 16 tokens between breaks and what is to be kept of them.  Loops are rolled: this
 // is rare, and straight-line code for it would be fetched anew each time.
 template <typename T>
 struct FwdRuns {
@@ -819,7 +820,7 @@ struct FwdRuns {
   int k, t0, ch;
   bool on;
   int serial;                              // the tile's number among those whose warps go one by one, 0: it is none
-  int from, end;                           // per lane q < 8: link of token t0 + q, its node if it is the node's last
+  int from, end;                           // per lane q < 16: link of token t0 + q, its node if it is the node's last
   uint32_t breaks, ends, reset;            // a bit a token; reset: breaks that start from outside the tile
   DEVI uint32_t behind(int q) const { return q < 31 ? ~((2u << q) - 1u) : 0u; }
   DEVI int run_end(int q) const {
@@ -911,14 +912,14 @@ struct FwdRuns {
 
 // The walking warps, forward.  Returns where a wait gave up or the tiles have ended.
 template <typename T>
-DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& kept, uint8_t* slots,
-                   int group, int warp, const WaitCtl& wc) {
+DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& kept, uint8_t* slots,
+                   int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t n_own = 0;                                  // uses of the walking warps' barriers so far
   int n_turn = 0;
   Tile t;
-  for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kFwdWalks) {
+  for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;          // the lane's first channel
     const int t0 = t.k * kTile + warp * kWarpTokens;
@@ -956,7 +957,7 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
       }
       last_known = f.known_runs(last);
       if (!serial) {                                   // every warp's map is there
-        if (f.breaks) sh_st(sh.B[t.s][warp * kFwdMaps], last);
+        if (f.breaks) sh_st(sh.B[t.s][warp], last);
         if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
         warp_arrive(&g.own);
         if (!wait_phase(&g.own, n_own & 1, wc)) return;
@@ -965,11 +966,8 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
     }
     // The state before the warp: from the maps of the warps before it; where a break starts from a node that
     // ends in this very tile, from the warp before it, which has then kept its nodes' states.
-    auto past = [&](int q, Vec<CH> v) {                // the state behind warp q's tokens, by their maps
-#pragma unroll
-      for (int m = 0; m < kFwdMaps; ++m)
-        v = vfma(sh_ld<CH>(sh.A[t.s][q * kFwdMaps + m]), v, sh_ld<CH>(sh.B[t.s][q * kFwdMaps + m]));
-      return v;
+    auto past = [&](int q, Vec<CH> v) {                // the state behind warp q's tokens, by their map
+      return vfma(sh_ld<CH>(sh.A[t.s][q]), v, sh_ld<CH>(sh.B[t.s][q]));
     };
     auto hand_on = [&](Vec<CH> v) {                    // to the warps and the tiles behind
       if (serial && warp < kScanWarps - 1) {
@@ -982,9 +980,9 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
     if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
     Vec<CH> h = sh_ld<CH>(sh.in[t.s]);
     if (t.info & kInfoMapped) {
-      h = vfma(sh_ld<CH>(sh.A[t.s][warp * kFwdMaps]), h, sh_ld<CH>(sh.B[t.s][warp * kFwdMaps]));
+      h = vfma(sh_ld<CH>(sh.A[t.s][warp]), h, sh_ld<CH>(sh.B[t.s][warp]));
     } else if (!serial) {
-      for (int q = 0; q < warp; ++q) h = sh.reset[t.s][q] ? sh_ld<CH>(sh.B[t.s][q * kFwdMaps]) : past(q, h);
+      for (int q = 0; q < warp; ++q) h = sh.reset[t.s][q] ? sh_ld<CH>(sh.B[t.s][q]) : past(q, h);
     } else if (warp > 0) {
       if (!wait_phase(&g.turn[warp], (n_turn - 1) & 1, wc)) return;
       h = sh_ld<CH>(g.carry[warp - 1]);
@@ -1017,9 +1015,9 @@ DEVI void fwd_walk(const ScanFwd<T>& a, FwdShared& sh, ScanWalk& g, ScanEnds& ke
   }
 }
 
-// The mapping warps, backward: p, and the 8-token maps of h and of the gradient (which share the factor).
+// The mapping warps, backward: p, and a warp's maps of h and of the gradient (which share the factor).
 template <typename T, int KIND>
-DEVI void bwd_map(BwdShared& sh, ScanBack& back, uint8_t* slots, int warp, const WaitCtl& wc) {
+DEVI void bwd_map(ScanShared& sh, ScanBack& back, uint8_t* slots, int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH;
   Tile t;
   for (int i = 0; next_tile(sh, sh.full, i, t, wc); ++i) {
@@ -1042,7 +1040,7 @@ DEVI void bwd_map(BwdShared& sh, ScanBack& back, uint8_t* slots, int warp, const
   }
 }
 
-// Backward, a warp at whose 8 tokens paths break or join.
+// Backward, a warp at whose 16 tokens paths break or join.
 template <typename T, int KIND>
 struct BwdBreaks {
   static constexpr int CH = Lane<T>::CH;
@@ -1050,7 +1048,7 @@ struct BwdBreaks {
   const Rows<T>& rows;
   int t0, ch;
   bool on;
-  int from, end, kid, sib, own;            // per lane q < 8, of token t0 + q; own: its node
+  int from, end, kid, sib, own;            // per lane q < 16, of token t0 + q; own: its node
   uint32_t breaks, joins;
   int kid_at, sib_at;                      // per lane: the token of this tile at which kid, sib starts; -1: in another
   // h before four tokens from g on; h: before token g, and on return behind the four
@@ -1090,14 +1088,14 @@ struct BwdBreaks {
 
 // The walking warps, backward: h before every token, then the gradients from the last token to the first.
 template <typename T, int KIND>
-DEVI void bwd_walk(const ScanBwd<T>& a, BwdShared& sh, ScanBack& back, ScanWalk& gr, uint8_t* slots,
-                   int group, int warp, const WaitCtl& wc) {
+DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk& gr, uint8_t* slots,
+                   int warp, const WaitCtl& wc) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   const int lane = threadIdx.x & 31;
   uint32_t n_own = 0;
   int n_turn = 0;
   Tile t;
-  for (int i = group; next_tile(sh, sh.told, i, t, wc); i += kBwdWalks) {
+  for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;
     const int t0 = t.k * kTile + warp * kWarpTokens;
@@ -1316,24 +1314,21 @@ constexpr int scan_smem(int slots) { return slots * kPlanes * kPlane + 128; }
 
 DEVI uint8_t* scan_align(uint8_t* p) { return p + ((128u - (smem_u32(p) & 127u)) & 127u); }   // copies land on 128 bytes
 
-template <int SLOTS, int MAPS, int WALKS>
-DEVI void scan_init(ScanShared<SLOTS, MAPS>& sh, ScanWalk (&walks)[WALKS]) {
+DEVI void scan_init(ScanShared& sh, ScanWalk& walk) {
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
-    for (int s = 0; s < SLOTS; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&sh.drawn[s], 1);
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.told[s], 1);
-      mbar_init(&sh.mapped[s], kScanWarps * MAPS);
+      mbar_init(&sh.mapped[s], kScanWarps);
       mbar_init(&sh.known[s], 1);
       mbar_init(&sh.ready[s], 1);
       mbar_init(&sh.empty[s], kScanWarps + 1);     // the walking warps and the joining warp
     }
-    for (int g = 0; g < WALKS; ++g) {
-      for (int q = 0; q < kTile; ++q) walks[g].row_of[q] = 0;
-      mbar_init(&walks[g].own, kScanWarps);
-      for (int q = 0; q < kScanWarps; ++q) mbar_init(&walks[g].turn[q], 1);
-    }
+    for (int q = 0; q < kTile; ++q) walk.row_of[q] = 0;
+    mbar_init(&walk.own, kScanWarps);
+    for (int q = 0; q < kScanWarps; ++q) mbar_init(&walk.turn[q], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncthreads();
@@ -1342,62 +1337,60 @@ DEVI void scan_init(ScanShared<SLOTS, MAPS>& sh, ScanWalk (&walks)[WALKS]) {
 // Every wait between warps is on an mbarrier and has a limit; the first that gives up raises the block's
 // abort flag, which ends the others.
 template <typename T, int KIND>
-__global__ void __launch_bounds__(scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), 1) k_scan_fwd(const __grid_constant__ CUtensorMap tm_gate,
+__global__ void __launch_bounds__(kScanThreads, 1) k_scan_fwd(const __grid_constant__ CUtensorMap tm_gate,
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const ScanFwd<T> a) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ FwdShared sh;
-  __shared__ ScanWalk walks[kFwdWalks];
-  __shared__ ScanEnds kept[kFwdWalks];
+  __shared__ ScanShared sh;
+  __shared__ ScanWalk walk;
+  __shared__ ScanEnds kept;
   uint8_t* slots = scan_align(smem_raw);
-  scan_init(sh, walks);
+  scan_init(sh, walk);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  constexpr int WALK = kFwdMaps * kScanWarps, LOAD = WALK + kFwdWalks * kScanWarps;     // first warp of each role
+  constexpr int WALK = kScanWarps, LOAD = 2 * kScanWarps;     // first warp of each role
   const int warp = threadIdx.x >> 5;
   if (warp < WALK) {
     fwd_map<T, KIND>(sh, slots, warp, wc);
   } else if (warp < LOAD) {
-    const int group = warp / kScanWarps - kFwdMaps;
-    fwd_walk<T>(a, sh, walks[group], kept[group], slots, group, warp % kScanWarps, wc);
+    fwd_walk<T>(a, sh, walk, kept, slots, warp - WALK, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
     scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
   } else if (warp == LOAD + 1) {
     fwd_publish<CH>(sh, a.w, a.C, SLAB, wc);
   } else {
-    scan_join<true, CH, kFwdJoins>(sh, a.w, a.C, a.t.n_tiles, a.states + (size_t)a.t.n_nodes * a.C, SLAB, false,
+    scan_join<true, CH>(sh, a.w, a.C, a.t.n_tiles, a.states + (size_t)a.t.n_nodes * a.C, SLAB, false,
                                    warp - LOAD - 2, wc);
   }
 }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), 1) k_scan_bwd(const __grid_constant__ CUtensorMap tm_gate,
+__global__ void __launch_bounds__(kScanThreads, 1) k_scan_bwd(const __grid_constant__ CUtensorMap tm_gate,
                                                               const __grid_constant__ CUtensorMap tm_x,
                                                               const __grid_constant__ CUtensorMap tm_dy,
                                                               const ScanBwd<T> a) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ uint8_t smem_raw[];
-  __shared__ BwdShared sh;
+  __shared__ ScanShared sh;
   __shared__ ScanBack back;
-  __shared__ ScanWalk walks[kBwdWalks];
+  __shared__ ScanWalk walk;
   uint8_t* slots = scan_align(smem_raw);
-  scan_init(sh, walks);
+  scan_init(sh, walk);
   const WaitCtl wc{&sh.abort_flag, a.status, a.limit_ns};
-  constexpr int WALK = kBwdMaps * kScanWarps, LOAD = WALK + kBwdWalks * kScanWarps;     // first warp of each role
+  constexpr int WALK = kScanWarps, LOAD = 2 * kScanWarps;     // first warp of each role
   const int warp = threadIdx.x >> 5;
   if (warp < WALK) {
     bwd_map<T, KIND>(sh, back, slots, warp, wc);
   } else if (warp < LOAD) {
-    const int group = warp / kScanWarps - kBwdMaps;
-    bwd_walk<T, KIND>(a, sh, back, walks[group], slots, group, warp % kScanWarps, wc);
+    bwd_walk<T, KIND>(a, sh, back, walk, slots, warp - WALK, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[3] = {&tm_gate, &tm_x, &tm_dy};
     scan_load<false>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
   } else if (warp == LOAD + 1) {
     bwd_publish<CH>(sh, back, a.w, a.states + (size_t)a.t.n_nodes * a.C, a.C, SLAB, wc);
   } else {
-    scan_join<false, CH, kBwdJoins>(sh, a.w, a.C, a.t.n_tiles, a.w.carry, SLAB, a.d_final != nullptr,
+    scan_join<false, CH>(sh, a.w, a.C, a.t.n_tiles, a.w.carry, SLAB, a.d_final != nullptr,
                                     warp - LOAD - 2, wc);
   }
 }
@@ -1578,7 +1571,7 @@ ScanTree scan_tree(const tree_plan_t* plan, const int32_t* parent, const int32_t
                   plan->n_tokens, plan->n_nodes,   scan_tiles(plan)};
 }
 
-// a tensor [N][C] in boxes of 64 tokens by a slab's channels; what lies outside reads as zero
+// a tensor [N][C] in boxes of a tile's tokens by a slab's channels; what lies outside reads as zero
 template <typename T>
 int scan_map(CUtensorMap* m, const void* base, int C, int N) {
   constexpr int box = kRow / (int)sizeof(T);
@@ -1626,7 +1619,7 @@ int run_fwd(const ScanFwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, c
   unsigned blocks = 0;
   const int rc = scan_grid<&k_scan_fwd<T, KIND>, scan_smem(kSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_fwd<T, KIND><<<blocks, scan_threads(kFwdMaps, kFwdWalks, kFwdJoins), scan_smem(kSlots), s>>>(tg, tx, a);
+  k_scan_fwd<T, KIND><<<blocks, kScanThreads, scan_smem(kSlots), s>>>(tg, tx, a);
   return record_cuda(cudaGetLastError());
 }
 template <typename T, int KIND>
@@ -1634,7 +1627,7 @@ int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, c
   unsigned blocks = 0;
   const int rc = scan_grid<&k_scan_bwd<T, KIND>, scan_smem(kSlots)>((int64_t)a.t.n_tiles * a.slabs, &blocks);
   if (rc) return rc;
-  k_scan_bwd<T, KIND><<<blocks, scan_threads(kBwdMaps, kBwdWalks, kBwdJoins), scan_smem(kSlots), s>>>(tg, tx, td, a);
+  k_scan_bwd<T, KIND><<<blocks, kScanThreads, scan_smem(kSlots), s>>>(tg, tx, td, a);
   return record_cuda(cudaGetLastError());
 }
 
