@@ -72,11 +72,11 @@ struct ScanTree {
 //   kid   for a node's last token: the second of the nodes that start from it (the first one is its
 //         successor in packed order), -1 if there is none
 //   sib   for a break: the next node after its own that starts from the same state, -1 if none
-// info: per tile, the kInfo bits.  flags: per tile and slab, whether its nodes' rows are written (those
-// that breaks start from; backward, those of its breaks).  ctl: the counter that hands out tiles (64
-// bits), and a word that stops every wait once one has run out of time.
+// info: per tile, the kInfo bits.  ctl: the counter that hands out tiles (64 bits), and a word that stops every
+// wait once one has run out of time.  dnode: per node that starts at a break, the gradient that it and the nodes
+// behind it hand to the state they start from.
 struct ScanWork {
-  int32_t *link, *end, *kid, *sib, *info, *flags, *ctl;
+  int32_t *link, *end, *kid, *sib, *info, *ctl;
   float *maps, *dnode, *carry;
 };
 
@@ -91,9 +91,10 @@ enum : int {
   kInfoMapped = 128,    // (set by the loading warp) the tile is a plain map of the state before it (gradient behind it)
   kInfoMap = 256,       // (the same) and other tiles join that map
 };
-// Maps and the states between tiles carry their own arrival: their rows hold this pattern, a NaN that no
-// arithmetic gives, until they are written, and whoever needs one polls the value itself.  No flag and no
-// fence stands between a tile and the next.
+// What tiles hand to one another carries its own arrival: the rows of maps, of the states between tiles, of nodes
+// that breaks start from (backward: dnode) hold this pattern, a NaN that no arithmetic gives, until they are written,
+// and whoever needs one polls the value itself.  No flag and no fence stands between a tile and the next: with
+// flags for the nodes' rows the 20011 x 1000 forest took 0.90 ms a step instead of 0.73.
 constexpr uint32_t kEmpty = 0xffffffffu;
 
 DEVI int scan_token_ancestor(int v, const ScanTree& t) {
@@ -111,12 +112,19 @@ DEVI int link_of(int j, const ScanTree& t) {
   return t.tok_start[a] + t.node_len[a] == j ? kLinkChain : a;
 }
 
-// Blocks (tile, share of the channels): links and info, the tile's flags cleared, its map and the state
-// behind it marked empty; and the rows that no tile writes are zeroed: those of nodes without tokens, and
-// with `inner` of nodes that do not start from nothing.
-__global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, int slabs, int C, int inner,
-                                                       float* rows, float* between) {
+// a node that a break starts from: its first child follows on it, a further one starts behind that
+DEVI bool is_source(int v, const ScanTree& t) {
+  const int next = t.tok_start[v] + t.node_len[v];
+  return next < t.sub_end[v] && t.sub_end[t.tok_node[next]] < t.sub_end[v];
+}
+
+// Blocks (tile, share of the channels): links and info; the tile's map and the state behind it marked empty.  FWD:
+// states of nodes that breaks start from marked empty, of nodes without tokens zeroed.  Backward: dnode of nodes
+// that start at a break from another's state marked empty, d_init of those that do not start from it zeroed.
+template <bool FWD>
+__global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, int C, float* rows, float* between) {
   __shared__ int bits;
+  __shared__ uint8_t marks[kTile];
   const int k = blockIdx.x, j = k * kTile + threadIdx.x;
   {
     const uint4 e = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
@@ -125,13 +133,33 @@ __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, 
     uint4* b = reinterpret_cast<uint4*>(between + (size_t)k * C);
     for (int i = first; i < C / 2; i += step) m[i] = e;
     for (int i = first; i < C / 4; i += step) b[i] = e;
-    for (int i = first; i < slabs; i += step) w.flags[(size_t)k * slabs + i] = 0;
-  }
-  if (rows)
-    for (int v = k; v < t.n_nodes; v += gridDim.x) {
-      if (t.node_len[v] > 0 && !(inner && scan_token_ancestor(v, t) >= 0)) continue;
-      for (int c = blockIdx.y * kTile + threadIdx.x; c < C; c += gridDim.y * kTile) rows[(size_t)v * C + c] = 0.f;
+    auto fill = [&](float* row, uint4 v) {
+      for (int i = first; i < C / 4; i += step) reinterpret_cast<uint4*>(row)[i] = v;
+    };
+    // a node a thread, then a row at a time
+    enum : uint8_t { kNone = 0, kRowEmpty = 1, kRowZero = 2 };
+    for (int v0 = k * kTile; v0 < t.n_nodes; v0 += gridDim.x * kTile) {
+      const int v = v0 + threadIdx.x;
+      uint8_t mark = kNone;
+      if (v < t.n_nodes) {
+        const bool some = t.node_len[v] > 0;
+        if (FWD) {
+          mark = !some ? kRowZero : is_source(v, t) ? kRowEmpty : kNone;
+        } else {
+          const int link = some ? link_of(t.tok_start[v], t) : kLinkChain;
+          mark = (link >= 0 ? kRowEmpty : kNone) | (rows && link != kLinkRoot ? kRowZero : kNone);
+        }
+      }
+      marks[threadIdx.x] = mark;
+      __syncthreads();
+      for (int q = 0; q < min(kTile, t.n_nodes - v0); ++q) {
+        const size_t at = (size_t)(v0 + q) * C;
+        if (marks[q] & kRowEmpty) fill((FWD ? rows : w.dnode) + at, e);
+        if (marks[q] & kRowZero) fill(rows + at, make_uint4(0, 0, 0, 0));
+      }
+      __syncthreads();
     }
+  }
   if (blockIdx.y) return;
   if (threadIdx.x == 0) bits = 0;
   if (k == 0 && threadIdx.x < 4) w.ctl[threadIdx.x] = 0;
@@ -446,11 +474,6 @@ DEVI bool wait_until(Look look, const WaitCtl& wc, int32_t* stop) {
     }
   }
 }
-// ... until a tile's node rows are written
-DEVI bool wait_rows(const int32_t* flag, const WaitCtl& wc, int32_t* stop) {
-  return wait_until([&] { return ld_acquire(flag) != 0; }, wc, stop);
-}
-
 DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, int c1) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
@@ -646,10 +669,11 @@ struct Rows {
   }
 };
 
-// The warp's writes so far, and those that a barrier ordered before them, become visible with the flag.
-DEVI void publish(int32_t* flag) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) set_release(flag, 1);
+// a row that another tile may still have to write: wait until it is there, after a first look at it in v
+template <int CH>
+DEVI bool arrived(const float* row, Vec<CH>& v, bool want, const WaitCtl& wc, int32_t* stop) {
+  if (!want || is_full(v)) return true;
+  return wait_until([&] { v = look_state(row, v); return is_full(v); }, wc, stop);
 }
 
 // The state before a tile (backward: the gradient behind it), from the state behind tile b and the maps of the
@@ -820,7 +844,9 @@ struct FwdRuns {
   int k, t0, ch;
   bool on;
   int serial;                              // the tile's number among those whose warps go one by one, 0: it is none
-  int from, end;                           // per lane q < 16: link of token t0 + q, its node if it is the node's last
+  // per lane q < 16: link of token t0 + q; its node if it is the node's last; its node; where in the tile the node that
+  // it starts from ends, -1 if elsewhere
+  int from, end, own, src;
   uint32_t breaks, ends, reset;            // a bit a token; reset: breaks that start from outside the tile
   DEVI uint32_t behind(int q) const { return q < 31 ? ~((2u << q) - 1u) : 0u; }
   DEVI int run_end(int q) const {
@@ -843,7 +869,7 @@ struct FwdRuns {
       }
       if (e < q1) {                        // a node's last token: its state, for the user and for breaks
         const int n = __shfl_sync(0xffffffffu, end, e), tok = t0 + e - k * kTile, slot = tok / kKeep;
-        if (on) st_state(a.states + (size_t)n * a.C + ch, h);
+        if (on) hand_state(a.states + (size_t)n * a.C + ch, h);
         if (serial) {
           // no token's while it changes: whoever reads it looks at the token afterwards
           if ((threadIdx.x & 31) == 0) *(volatile int*)&kept.token[slot] = -1;
@@ -859,32 +885,83 @@ struct FwdRuns {
     }
     return h;
   }
-  // All runs that start from outside the tile, which wait for nothing here: true if the last run is one of them,
-  // whose end is then the state behind the warp.
-  DEVI bool known_runs(Vec<CH>& last) const {
+  // where the run that starts at token q begins, n its link
+  DEVI const float* start_row(int q, int n) const {
+    const int v = __shfl_sync(0xffffffffu, own, q);
+    return n >= 0 ? a.states + (size_t)n * a.C : (a.init && n == kLinkRoot ? a.init + (size_t)v * a.C : nullptr);
+  }
+  // all initial states on their way at once
+  DEVI void fetch_init() const {
+    if (!a.init) return;
+#pragma unroll 4
+    for (int q = 0; q < kWarpTokens; ++q) {
+      const int n = __shfl_sync(0xffffffffu, from, q), v = __shfl_sync(0xffffffffu, own, q);
+      if (on && n == kLinkRoot) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.init + (size_t)v * a.C + ch));
+    }
+  }
+  // Every token of the warp is such a run of its own (a step of many sequences: 4096 by 4096 channels in 103 us,
+  // 187 run by run); h: the last one's state.
+  DEVI bool single_runs(Vec<CH>& h, const WaitCtl& wc) const {
+    bool ok = true;
+    fetch_init();
+#pragma unroll 1
+    for (int g = 0; g < kWarpTokens && t0 + g < a.t.N; g += 4) {
+      Vec<CH> s[4];
+      int n[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        n[r] = __shfl_sync(0xffffffffu, from, g + r);
+        const float* row = start_row(g + r, n[r]);
+        s[r] = ld_state_if(row + ch, on && row, h);
+      }
+      T* y = a.y + (size_t)(t0 + g) * a.C + ch;
+#pragma unroll
+      for (int r = 0; r < 4; ++r, y += a.C) {
+        if (t0 + g + r >= a.t.N) break;
+        ok = arrived(a.states + (size_t)n[r] * a.C + ch, s[r], on && n[r] >= 0, wc, a.w.ctl + 2) && ok;
+        h = rows.step(g + r, s[r]);
+        const int e = __shfl_sync(0xffffffffu, end, g + r);
+        if (on) {
+          *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
+          if (e >= 0) hand_state(a.states + (size_t)e * a.C + ch, h);
+        }
+      }
+    }
+    return __all_sync(0xffffffffu, ok);
+  }
+  // All runs that start from outside the tile, which wait for nothing in it.  `known`: the last run is one of them,
+  // whose end is then the state behind the warp.  False if a wait gave up.
+  DEVI bool known_runs(Vec<CH>& last, bool& known, const WaitCtl& wc) const {
+    if (reset && !serial && reset == (1u << min(kWarpTokens, a.t.N - t0)) - 1u) {
+      known = true;
+      return single_runs(last, wc);
+    }
 #pragma unroll 1
     for (uint32_t m = reset; m;) {
       // the starts of four runs at a time: their loads are in flight together
       Vec<CH> s[4];
-      int q[4];
+      int q[4], n[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         q[r] = m ? __ffs(m) - 1 : -1;
         m &= m - 1;
-        const int n = __shfl_sync(0xffffffffu, from, max(q[r], 0));
-        const float* row = n >= 0 ? a.states + (size_t)n * a.C
-                                  : (a.init && q[r] >= 0 ? a.init + (size_t)a.t.tok_node[t0 + q[r]] * a.C : nullptr);
+        n[r] = __shfl_sync(0xffffffffu, from, max(q[r], 0));
+        const float* row = start_row(max(q[r], 0), n[r]);
         s[r] = ld_state_if(row + ch, on && row && q[r] >= 0, last);
       }
 #pragma unroll 1
       for (int r = 0; r < 4; ++r) {
         if (q[0] < 0) break;
+        const bool ok = arrived(a.states + (size_t)n[0] * a.C + ch, s[0], on && n[0] >= 0, wc, a.w.ctl + 2);
+        if (!__all_sync(0xffffffffu, ok)) return false;
         last = run(s[0], q[0]);
         s[0] = s[1]; s[1] = s[2]; s[2] = s[3];
         q[0] = q[1]; q[1] = q[2]; q[2] = q[3]; q[3] = -1;
+        n[0] = n[1]; n[1] = n[2]; n[2] = n[3];
       }
     }
-    return reset && (breaks >> (31 - __clz(reset))) == 1u;
+    known = reset && (breaks >> (31 - __clz(reset))) == 1u;
+    return true;
   }
   // The runs that wait: the one that comes into the warp, and those that start from nodes of this tile.  v: the
   // state behind the last of them; false if a wait gave up.
@@ -893,7 +970,7 @@ struct FwdRuns {
 #pragma unroll 1
     for (uint32_t m = breaks & ~reset; m; m &= m - 1) {
       const int q = __ffs(m) - 1, n = __shfl_sync(0xffffffffu, from, q);
-      const int tok = a.t.tok_start[n] + a.t.node_len[n] - 1 - k * kTile, slot = tok / kKeep;
+      const int tok = __shfl_sync(0xffffffffu, src, q), slot = tok / kKeep;
       const bool ok = wait_until([&] { return *(volatile int*)&walk.row_of[tok] == serial; }, wc, a.w.ctl + 2);
       if (!__all_sync(0xffffffffu, ok)) return false;
       __threadfence_block();
@@ -925,26 +1002,21 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
     const int t0 = t.k * kTile + warp * kWarpTokens;
     const bool serial = t.info & kInfoSerial;
     n_turn += serial;
-    FwdRuns<T> f{a, rows, g, kept, t.k, t0, ch, ch < a.C, serial ? n_turn : 0, kLinkChain, -1, 0u, 0u, 0u};
+    FwdRuns<T> f{a, rows, g, kept, t.k, t0, ch, ch < a.C, serial ? n_turn : 0, kLinkChain, -1, 0, -1, 0u, 0u, 0u};
     const bool special = t.info & (kInfoBreak | kInfoEnd);
     if (special) {
-      bool ok = true, tile = false;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
         f.from = a.w.link[t0 + lane];
         f.end = a.w.end[t0 + lane];
+        f.own = a.t.tok_node[t0 + lane];
         if (f.from >= 0) {
-          const int ts = (a.t.tok_start[f.from] + a.t.node_len[f.from] - 1) / kTile;
-          tile = ts == t.k;
-          if (!tile) ok = wait_rows(a.w.flags + (size_t)ts * a.slabs + t.slab, wc, a.w.ctl + 2);
+          const int at = a.t.tok_start[f.from] + a.t.node_len[f.from] - 1;
+          if (at / kTile == t.k) f.src = at % kTile;
         }
-      }
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) sh.abort_flag = 1;
-        return;
       }
       f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
       f.ends = __ballot_sync(0xffffffffu, f.end >= 0);
-      f.reset = f.breaks & ~__ballot_sync(0xffffffffu, tile);
+      f.reset = f.breaks & ~__ballot_sync(0xffffffffu, f.src >= 0);
     }
     Vec<CH> last = vec<CH>(0.f);                       // the state behind the warp
     bool last_known = false;
@@ -955,7 +1027,10 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
         if (!wait_phase(&g.own, n_own & 1, wc)) return;
         ++n_own;
       }
-      last_known = f.known_runs(last);
+      if (!f.known_runs(last, last_known, wc)) {
+        if (lane == 0) sh.abort_flag = 1;
+        return;
+      }
       if (!serial) {                                   // every warp's map is there
         if (f.breaks) sh_st(sh.B[t.s][warp], last);
         if (lane == 0) sh.reset[t.s][warp] = f.breaks != 0;
@@ -977,13 +1052,20 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
       if (warp == kScanWarps - 1 && f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
     };
     if (last_known) hand_on(last);
-    if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
-    Vec<CH> h = sh_ld<CH>(sh.in[t.s]);
-    if (t.info & kInfoMapped) {
+    Vec<CH> h = vec<CH>(0.f);
+    if (f.breaks & 1u) {
+      // nothing comes into the warp (a turn that it does not take is over when the warps meet in the next such tile)
+    } else if (!wait_phase(&sh.ready[t.s], t.parity, wc)) {
+      return;
+    } else if (t.info & kInfoMapped) {
+      h = sh_ld<CH>(sh.in[t.s]);
       h = vfma(sh_ld<CH>(sh.A[t.s][warp]), h, sh_ld<CH>(sh.B[t.s][warp]));
     } else if (!serial) {
+      h = sh_ld<CH>(sh.in[t.s]);
       for (int q = 0; q < warp; ++q) h = sh.reset[t.s][q] ? sh_ld<CH>(sh.B[t.s][q]) : past(q, h);
-    } else if (warp > 0) {
+    } else if (warp == 0) {
+      h = sh_ld<CH>(sh.in[t.s]);
+    } else {
       if (!wait_phase(&g.turn[warp], (n_turn - 1) & 1, wc)) return;
       h = sh_ld<CH>(g.carry[warp - 1]);
     }
@@ -1004,12 +1086,6 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
         h = rows.step(q, h);
         if (q < rest) *reinterpret_cast<uint32_t*>(y) = Lane<T>::pack(h);
       }
-    }
-    if (t.info & kInfoSource) {                        // breaks elsewhere start from nodes that end here
-      warp_arrive(&g.own);
-      if (!wait_phase(&g.own, n_own & 1, wc)) return;
-      ++n_own;
-      if (warp == 0) publish(a.w.flags + (size_t)t.k * a.slabs + t.slab);
     }
     warp_arrive(&sh.empty[t.s]);
   }
@@ -1046,7 +1122,7 @@ struct BwdBreaks {
   static constexpr int CH = Lane<T>::CH;
   const ScanBwd<T>& a;
   const Rows<T>& rows;
-  int t0, ch;
+  int t0, tok0, ch;                        // tok0: t0's place in the tile
   bool on;
   int from, end, kid, sib, own;            // per lane q < 16, of token t0 + q; own: its node
   uint32_t breaks, joins;
@@ -1068,21 +1144,32 @@ struct BwdBreaks {
       h = advance<KIND>(rows.p(g + q), rows.get(1, g + q), b[q]);
     }
   }
+  // the kid of token q, -1 where there is none or it starts in these very four tokens
+  DEVI int kid_behind(int q) const {
+    const int kd = __shfl_sync(0xffffffffu, kid, q), at = __shfl_sync(0xffffffffu, kid_at, q);
+    return at >= 0 && (tok0 + q) / 4 == at / 4 ? -1 : kd;
+  }
   // dy of four tokens and what joins it: kid: the next node that starts from this one's state, with those behind
-  // it; end: the node's own final state
-  DEVI void sums(int g, Vec<CH> (&d)[4]) const {
+  // it; end: the node's own final state.  False if a wait gave up.
+  DEVI bool sums(int g, Vec<CH> (&d)[4], const WaitCtl& wc) const {
 #pragma unroll
     for (int q = 0; q < 4; ++q) d[q] = rows.get(2, g + q);
-    if (!((joins >> g) & 15u)) return;
+    if (!((joins >> g) & 15u)) return true;
     Vec<CH> f[4], k[4];
+    bool ok = true;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int kd = __shfl_sync(0xffffffffu, kid, g + q), e = __shfl_sync(0xffffffffu, end, g + q);
+      const int kd = kid_behind(g + q), e = __shfl_sync(0xffffffffu, end, g + q);
       f[q] = ld_state_if(a.d_final + (size_t)e * a.C + ch, on && a.d_final && e >= 0, d[q]);
       k[q] = ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on && kd >= 0, d[q]);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) d[q] = d[q] + (f[q] + k[q]);
+    for (int q = 0; q < 4; ++q) {
+      const int kd = kid_behind(g + q);
+      ok = arrived(a.w.dnode + (size_t)kd * a.C + ch, k[q], on && kd >= 0, wc, a.w.ctl + 2) && ok;
+      d[q] = d[q] + (f[q] + k[q]);
+    }
+    return __all_sync(0xffffffffu, ok);
   }
 };
 
@@ -1099,15 +1186,13 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
     const Rows<T> rows(slots, t.s, warp);
     const int ch = t.slab * SLAB + lane * CH;
     const int t0 = t.k * kTile + warp * kWarpTokens;
-    int32_t* flag = a.w.flags + (size_t)t.k * a.slabs + t.slab;
     const bool mapped = t.info & kInfoMapped, serial = t.info & kInfoSerialBack;
-    BwdBreaks<T, KIND> f{a, rows, t0, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u, -1, -1};
+    BwdBreaks<T, KIND> f{a, rows, t0, warp * kWarpTokens, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u, -1, -1};
     n_turn += serial;
     const bool on = f.on;
     Vec<CH> h = vec<CH>(0.f);
     if (!mapped) {
       h = ld_state_if(a.states + (size_t)(a.t.n_nodes + t.k - 1) * a.C + ch, on && (t.info & kInfoIn), h);
-      bool ok = true;
       if (lane < kWarpTokens && t0 + lane < a.t.N) {
         const int j = t0 + lane;
         f.from = a.w.link[j];
@@ -1115,20 +1200,9 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
         f.kid = a.w.kid[j];
         f.sib = a.w.sib[j];
         f.own = a.t.tok_node[j];
-        if (f.kid >= 0) {
-          const int tk = a.t.tok_start[f.kid] / kTile;
-          if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
-          else f.kid_at = a.t.tok_start[f.kid] - t.k * kTile;
-        }
-        if (ok && f.sib >= 0) {
-          const int tk = a.t.tok_start[f.sib] / kTile;
-          if (tk != t.k) ok = wait_rows(a.w.flags + (size_t)tk * a.slabs + t.slab, wc, a.w.ctl + 2);
-          else f.sib_at = a.t.tok_start[f.sib] - t.k * kTile;
-        }
-      }
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) sh.abort_flag = 1;
-        return;
+        // (a kid or sib in this tile: its first token there)
+        if (f.kid >= 0 && a.t.tok_start[f.kid] / kTile == t.k) f.kid_at = a.t.tok_start[f.kid] - t.k * kTile;
+        if (f.sib >= 0 && a.t.tok_start[f.sib] / kTile == t.k) f.sib_at = a.t.tok_start[f.sib] - t.k * kTile;
       }
       f.breaks = __ballot_sync(0xffffffffu, f.from != kLinkChain);
       f.joins = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
@@ -1138,6 +1212,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
     const int known = f.breaks ? (__ffs(f.breaks) - 1) & ~3 : kWarpTokens - 4;
     const bool near = __any_sync(0xffffffffu, f.kid_at >= 0);         // a node of this tile joins in the warp
     if (!wait_phase(mapped ? &sh.known[t.s] : &sh.mapped[t.s], t.parity, wc)) return;
+    bool ok = true;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
         Vec<CH> v = vec<CH>(0.f), b[4];
@@ -1152,7 +1227,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
         Vec<CH> R = vec<CH>(0.f), d[4];
 #pragma unroll 1
         for (int g = known; g >= 0; g -= 4) {
-          f.sums(g, d);
+          ok = f.sums(g, d, wc) && ok;
 #pragma unroll
           for (int q = 3; q >= 0; --q) {
             R = decayed(rows.p(g + q), d[q] + R);
@@ -1207,7 +1282,6 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
     }
     // a warp in which nothing of this tile joins hands on by its map, before it walks
     if (!mapped && !f.breaks && !near) hand_on(vfma(sh_ld<CH>(sh.A[t.s][warp]), u, sh_ld<CH>(back.R[t.s][warp])));
-    bool ok = true;
     auto wait_row = [&](int tok) {                     // of a node that starts in this tile
       const bool there = wait_until([&] { return *(volatile int*)&gr.row_of[tok] == n_turn; }, wc, a.w.ctl + 2);
       ok = __all_sync(0xffffffffu, there) && ok;
@@ -1267,9 +1341,9 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
         f.befores(g, h, b);
         for (uint32_t m = near ? (f.joins >> g) & 15u : 0u; m; m &= m - 1) {
           const int at = __shfl_sync(0xffffffffu, f.kid_at, g + __ffs(m) - 1);
-          if (at >= 0 && (at - warp * kWarpTokens) / 4 != g / 4) wait_row(at);      // (those of these four: below)
+          if (at >= 0 && at / 4 != (f.tok0 + g) / 4) wait_row(at);                  // (those of these four: below)
         }
-        f.sums(g, d);
+        ok = f.sums(g, d, wc) && ok;
 #pragma unroll
         for (int q = 3; q >= 0; --q) {
           const int kd = __shfl_sync(0xffffffffu, f.kid, g + q);
@@ -1286,8 +1360,10 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
             const int sb = __shfl_sync(0xffffffffu, f.sib, g + q);
             const int sb_at = __shfl_sync(0xffffffffu, f.sib_at, g + q);
             if (sb_at >= 0) wait_row(sb_at);
-            const Vec<CH> later = ld_state_if(a.w.dnode + (size_t)sb * a.C + ch, on && sb >= 0, u);
-            if (on && n >= 0) st_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
+            const float* row = a.w.dnode + (size_t)sb * a.C + ch;
+            Vec<CH> later = ld_state_if(row, on && sb >= 0, u);
+            ok = __all_sync(0xffffffffu, arrived(row, later, on && sb >= 0, wc, a.w.ctl + 2)) && ok;
+            if (on && n >= 0) hand_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
             if (on && n == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
             u = vec<CH>(0.f);
             if (serial) row_written(gr, warp * kWarpTokens + g + q, n_turn);
@@ -1300,12 +1376,6 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
       return;
     }
     if (near) hand_on(u);
-    if (!mapped && (t.info & kInfoBreak)) {
-      warp_arrive(&gr.own);
-      if (!wait_phase(&gr.own, n_own & 1, wc)) return;
-      ++n_own;
-      if (warp == 0) publish(flag);
-    }
     warp_arrive(&sh.empty[t.s]);
   }
 }
@@ -1525,7 +1595,7 @@ int scan_slabs(int C, int dtype) {
 }
 
 struct ScanLayout {
-  size_t link, end, kid, sib, info, flags, ctl, maps, dnode, carry, total;
+  size_t link, end, kid, sib, info, ctl, maps, dnode, carry, total;
 };
 
 ScanLayout scan_layout(const tree_plan_t* p, int C) {
@@ -1537,7 +1607,6 @@ ScanLayout scan_layout(const tree_plan_t* p, int C) {
   L.kid = o;   o += tok;
   L.sib = o;   o += tok;
   L.info = o;  o = align256(o + tiles * 4);
-  L.flags = o; o = align256(o + tiles * scan_slabs(C, TREE_F32) * 4);
   L.ctl = o;   o = align256(o + 16);
   L.maps = o;  o = align256(o + tiles * C * 8);
   L.dnode = o; o = align256(o + (size_t)p->n_nodes * C * 4);
@@ -1550,7 +1619,7 @@ ScanWork scan_work(void* workspace, const ScanLayout& L) {
   uint8_t* w = static_cast<uint8_t*>(workspace);
   auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(w + o); };
   auto f32 = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
-  return ScanWork{i32(L.link), i32(L.end), i32(L.kid), i32(L.sib), i32(L.info), i32(L.flags), i32(L.ctl),
+  return ScanWork{i32(L.link), i32(L.end), i32(L.kid), i32(L.sib), i32(L.info), i32(L.ctl),
                   f32(L.maps), f32(L.dnode), f32(L.carry)};
 }
 
@@ -1643,7 +1712,7 @@ int scan_fwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<prepare_grid(t, C), kTile, 0, s>>>(t, w, slabs, C, 0, states, states + (size_t)t.n_nodes * C);
+  k_scan_prepare<true><<<prepare_grid(t, C), kTile, 0, s>>>(t, w, C, states, states + (size_t)t.n_nodes * C);
   return kind == TREE_GATE_SIGMOID ? run_fwd<T, TREE_GATE_SIGMOID>(a, tg, tx, s)
                                    : run_fwd<T, TREE_GATE_LOG>(a, tg, tx, s);
 }
@@ -1658,7 +1727,7 @@ int scan_bwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (!rc) rc = scan_map<T>(&td, dy, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<<<prepare_grid(t, C), kTile, 0, s>>>(t, w, slabs, C, 1, d_init, w.carry);
+  k_scan_prepare<false><<<prepare_grid(t, C), kTile, 0, s>>>(t, w, C, d_init, w.carry);
   const ScanBwd<T> a{init, states, d_final, static_cast<T*>(dgate), static_cast<T*>(dx), d_init, t, w, C, slabs, status,
                      wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_bwd<T, TREE_GATE_SIGMOID>(a, tg, tx, td, s)
