@@ -483,8 +483,7 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
 }
 
 // A block works on up to kSlots tiles at a time, in the order in which it drew them:
-//   loading warp      draws a tile, starts its copies                                       -> drawn, full
-//   joining warp      looks up what the tile holds                                          -> told
+//   loading warp      draws a tile, starts its copies, looks up what it holds               -> full, told
 //   mapping warps     the map of every token (backward: its p) and of every warp's tokens    -> mapped
 //   publishing warp   joins the warps' maps to the tile's, hands that to the other blocks    -> known
 //   joining warp      finds the state before the tile, hands on the one behind it            -> ready
@@ -492,8 +491,9 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
 // So a tile whose state is late holds up nothing that another tile waits for: its map is out, and so are
 // those of the tiles that the block drew after it.
 struct ScanShared {
-  uint64_t drawn[kSlots], full[kSlots], told[kSlots], mapped[kSlots], known[kSlots], ready[kSlots], empty[kSlots];
+  uint64_t full[kSlots], told[kSlots], mapped[kSlots], known[kSlots], ready[kSlots], empty[kSlots];
   int tile[kSlots], slab[kSlots], info[kSlots];
+  int dist[kSlots];                                // maps between the tile and the state that it starts from
   int abort_flag;
   int reset[kSlots][kScanWarps];
   // Per warp and channel the map of its tokens; in a tile without breaks the publishing warp puts that of all
@@ -557,7 +557,7 @@ struct ScanBwd {
 // The loading warp: draws tiles from the counter and starts their copies.
 template <bool FWD, int TENSORS>
 DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
-                    int tiles, int slabs, int slab_ch, const WaitCtl& wc) {
+                    int tiles, int slabs, int slab_ch, bool joins, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   auto draw = [&] { return atomicAdd(reinterpret_cast<unsigned long long*>(w.ctl), 1ull); };
   unsigned long long next = lane == 0 ? draw() : 0;
@@ -571,7 +571,6 @@ DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&t
     if (turn >= (unsigned)tiles) {                   // the end, for all that take tiles in turn
       if (lane == 0) {
         sh.tile[s] = -1;
-        mbar_arrive(&sh.drawn[s]);
         mbar_arrive(&sh.told[s]);
         mbar_arrive(&sh.full[s]);
       }
@@ -583,11 +582,23 @@ DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&t
     if (lane == 0) {
       sh.tile[s] = k;
       sh.slab[s] = slab;
-      mbar_arrive(&sh.drawn[s]);
       mbar_expect_tx(&sh.full[s], TENSORS * kPlane);
 #pragma unroll
       for (int a = 0; a < TENSORS; ++a)
         tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * kTile);
+    }
+    // what the tile holds, and what the tiles before it (backward: behind it) do
+    const int n = FWD ? k - lane : k + lane;
+    int info = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
+    // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
+    const bool mapped = !(info & kInfoBreak) && (FWD || !(info & kInfoSource || (joins && (info & kInfoEnd))));
+    const bool map = mapped && (FWD ? (n + 1) % kScanGroup != 0 : (info & kInfoOut) && n % kScanGroup != 0);
+    const uint32_t run = __ballot_sync(0xffffffffu, map);
+    info = __shfl_sync(0xffffffffu, info | (mapped ? kInfoMapped : 0) | (map ? kInfoMap : 0), 0);
+    if (lane == 0) {
+      sh.info[s] = info;
+      sh.dist[s] = __ffs(~(run >> 1)) - 1;
+      mbar_arrive(&sh.told[s]);
     }
     // The first tiles are drawn one at a time, so that neighbours go to different blocks; later ones ahead.
     if (i + 1 < kSlots && !wait_phase(&sh.full[s], 0, wc)) {
@@ -772,26 +783,17 @@ DEVI void bwd_publish(ScanShared& sh, ScanBack& back, const ScanWork& w, const f
   }
 }
 
-// A joining warp.  It finds how many maps lie between the tile and the state it starts from.  FWD: that is the
+// A joining warp.  `dist` maps lie between the tile and the state it starts from.  FWD: that is the
 // state behind the nearest tile before it that is no plain map or ends a group of kScanGroup; backward the same
 // from the other side.  Groups bound the maps that a tile joins; within one, no tile waits for a state to be
 // handed on.  rows: the states between tiles (backward: the gradients).
 template <bool FWD, int CH>
-DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, int tiles, float* rows, int slab_ch, bool joins,
-                    int joiner, const WaitCtl& wc) {
+DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, float* rows, int slab_ch, int joiner,
+                    const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
-  for (int i = joiner; next_tile(sh, sh.drawn, i, t, wc); i += kJoins) {
-    const int n = FWD ? t.k - lane : t.k + lane;
-    int info = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
-    // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
-    const bool mapped = !(info & kInfoBreak) && (FWD || !(info & kInfoSource || (joins && (info & kInfoEnd))));
-    const bool map = mapped && (FWD ? (n + 1) % kScanGroup != 0 : (info & kInfoOut) && n % kScanGroup != 0);
-    const uint32_t run = __ballot_sync(0xffffffffu, map);
-    info = __shfl_sync(0xffffffffu, info | (mapped ? kInfoMapped : 0) | (map ? kInfoMap : 0), 0);
-    if (lane == 0) sh.info[t.s] = info;
-    warp_arrive(&sh.told[t.s]);
-    const int ch = t.slab * slab_ch + lane * CH, dist = __ffs(~(run >> 1)) - 1;
+  for (int i = joiner; next_tile(sh, sh.told, i, t, wc); i += kJoins) {
+    const int info = t.info, ch = t.slab * slab_ch + lane * CH, dist = sh.dist[t.s];
     const bool on = ch < C, need = info & (FWD ? kInfoIn : kInfoOut);
     const int b = FWD ? t.k - 1 - dist : t.k + 1 + dist;
     const Joiner<CH> j{w, C, ch, b, FWD ? 1 : -1, dist, rows + (size_t)(need ? b : 0) * C + ch, on};
@@ -1388,7 +1390,6 @@ DEVI void scan_init(ScanShared& sh, ScanWalk& walk) {
   if (threadIdx.x == 0) {
     sh.abort_flag = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(&sh.drawn[s], 1);
       mbar_init(&sh.full[s], 1);
       mbar_init(&sh.told[s], 1);
       mbar_init(&sh.mapped[s], kScanWarps);
@@ -1426,11 +1427,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_fwd(const __grid_const
     fwd_walk<T>(a, sh, walk, kept, slots, warp - WALK, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
-    scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
+    scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, false, wc);
   } else if (warp == LOAD + 1) {
     fwd_publish<CH>(sh, a.w, a.C, SLAB, wc);
   } else {
-    scan_join<true, CH>(sh, a.w, a.C, a.t.n_tiles, a.states + (size_t)a.t.n_nodes * a.C, SLAB, false,
+    scan_join<true, CH>(sh, a.w, a.C, a.states + (size_t)a.t.n_nodes * a.C, SLAB,
                                    warp - LOAD - 2, wc);
   }
 }
@@ -1456,11 +1457,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_bwd(const __grid_const
     bwd_walk<T, KIND>(a, sh, back, walk, slots, warp - WALK, wc);
   } else if (warp == LOAD) {
     const CUtensorMap* tm[3] = {&tm_gate, &tm_x, &tm_dy};
-    scan_load<false>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, wc);
+    scan_load<false>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, a.d_final != nullptr, wc);
   } else if (warp == LOAD + 1) {
     bwd_publish<CH>(sh, back, a.w, a.states + (size_t)a.t.n_nodes * a.C, a.C, SLAB, wc);
   } else {
-    scan_join<false, CH>(sh, a.w, a.C, a.t.n_tiles, a.w.carry, SLAB, a.d_final != nullptr,
+    scan_join<false, CH>(sh, a.w, a.C, a.w.carry, SLAB,
                                     warp - LOAD - 2, wc);
   }
 }
