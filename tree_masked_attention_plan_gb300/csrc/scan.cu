@@ -20,11 +20,12 @@
 // change from run to run.
 //
 // Measured (bf16, 268M elements, sigmoid gate): one sequence of 32768 tokens by 8192 channels forward
-// 0.34 ms, 4.7 TB/s, backward 0.61 ms, 4.4 TB/s; a tree of the same size (nodes of some 250 tokens) 0.41 and
-// 0.77 ms.  What bounds it there is instruction issue and the dependent steps of a warp's walk (in the backward a
+// 0.34 ms, 4.8 TB/s, backward 0.59 ms, 4.5 TB/s; a tree of the same size (nodes of some 250 tokens) 0.39 and
+// 0.74 ms.  What bounds it there is instruction issue and the dependent steps of a warp's walk (in the backward a
 // step of 64 channels takes 120 instructions, and the SM issues in 57 % of all cycles; the copies alone, without
-// the arithmetic, take 0.27 ms in the forward).  In a tree of short nodes it is the way of a state through the
-// tiles, one after the other: 3456 tokens of a caterpillar by 4096 channels take 103 us, 13 at the memory's rate.
+// the arithmetic, take 0.27 ms in the forward).  In a tree of short nodes or of few channels it is the way of a
+// state through the tiles, one after the other: 3456 tokens of a caterpillar by 4096 channels take 97 us, 13 at the
+// memory's rate.
 // Why 128 tokens: a tile hands on 4 bytes of state and 8 of map for each channel, and one of 64 tokens twice as
 // often (the tree: 0.53 instead of 0.42 ms forward, 1.00 instead of 0.78 backward).
 //
@@ -72,11 +73,11 @@ struct ScanTree {
 //   kid   for a node's last token: the second of the nodes that start from it (the first one is its
 //         successor in packed order), -1 if there is none
 //   sib   for a break: the next node after its own that starts from the same state, -1 if none
-// info: per tile, the kInfo bits.  ctl: the counter that hands out tiles (64 bits), and a word that stops every
+// info, edge: per tile, the kInfo bits; its first and last break (bits 0-7, 8-15).  ctl: the counter that hands out tiles (64 bits), and a word that stops every
 // wait once one has run out of time.  dnode: per node that starts at a break, the gradient that it and the nodes
 // behind it hand to the state they start from.
 struct ScanWork {
-  int32_t *link, *end, *kid, *sib, *info, *ctl;
+  int32_t *link, *end, *kid, *sib, *info, *edge, *ctl;
   float *maps, *dnode, *carry;
 };
 
@@ -90,6 +91,9 @@ enum : int {
   kInfoSerialBack = 64, // a node's further child, or a break's next sibling, starts in this tile
   kInfoMapped = 128,    // (set by the loading warp) the tile is a plain map of the state before it (gradient behind it)
   kInfoMap = 256,       // (the same) and other tiles join that map
+  kInfoLast = 512,      // its last break starts from outside the tile
+  kInfoFirst = 1024,    // nothing joins before its first break but nodes' final states
+  kInfoFirstEnd = 2048, // a node ends before its first break
 };
 // What tiles hand to one another carries its own arrival: the rows of maps, of the states between tiles, of nodes
 // that breaks start from (backward: dnode) hold this pattern, a NaN that no arithmetic gives, until they are written,
@@ -123,7 +127,7 @@ DEVI bool is_source(int v, const ScanTree& t) {
 // that start at a break from another's state marked empty, d_init of those that do not start from it zeroed.
 template <bool FWD>
 __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, int C, float* rows, float* between) {
-  __shared__ int bits;
+  __shared__ int bits, lo, hi;
   __shared__ uint8_t marks[kTile];
   const int k = blockIdx.x, j = k * kTile + threadIdx.x;
   {
@@ -161,17 +165,29 @@ __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, 
     }
   }
   if (blockIdx.y) return;
-  if (threadIdx.x == 0) bits = 0;
+  if (threadIdx.x == 0) {
+    bits = 0;
+    lo = kTile;
+    hi = -1;
+  }
   if (k == 0 && threadIdx.x < 4) w.ctl[threadIdx.x] = 0;
   __syncthreads();
+  int mine = 0, kid = -1, end = -1;
+  bool outside = true;
   if (j < t.N) {
     const int v = t.tok_node[j];
     const int link = link_of(j, t);
-    int sib = -1, end = -1, kid = -1, mine = 0;
-    if (link != kLinkChain) mine |= kInfoBreak;
-    else if (threadIdx.x == 0) mine |= kInfoIn;
+    int sib = -1;
+    if (link != kLinkChain) {
+      mine |= kInfoBreak;
+      atomicMin(&lo, (int)threadIdx.x);
+      atomicMax(&hi, (int)threadIdx.x);
+    } else if (threadIdx.x == 0) mine |= kInfoIn;
     if (link >= 0) {
-      if ((t.tok_start[link] + t.node_len[link] - 1) / kTile == k) mine |= kInfoSerial;
+      if ((t.tok_start[link] + t.node_len[link] - 1) / kTile == k) {
+        mine |= kInfoSerial;
+        outside = false;
+      }
       const int next = t.sub_end[v];
       if (next < t.sub_end[link]) {
         sib = t.tok_node[next];
@@ -195,10 +211,16 @@ __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, 
     w.end[j] = end;
     w.kid[j] = kid;
     w.sib[j] = sib;
-    if (mine) atomicOr(&bits, mine);
   }
   __syncthreads();
-  if (threadIdx.x == 0) w.info[k] = bits;
+  if ((int)threadIdx.x == hi && outside) mine |= kInfoLast;
+  if ((int)threadIdx.x < lo && end >= 0) mine |= kInfoFirstEnd;
+  if (mine) atomicOr(&bits, mine);
+  const bool kids = __syncthreads_or((int)threadIdx.x < lo && kid >= 0);
+  if (threadIdx.x == 0) {
+    w.info[k] = bits | (hi >= 0 && !kids ? kInfoFirst : 0);
+    w.edge[k] = (lo & 255) | (max(hi, 0) << 8);
+  }
 }
 
 // A lane's one or two channels of a value; pairs go through the packed fp32 instructions.
@@ -485,7 +507,8 @@ DEVI void tma_load_2d(void* dst, const CUtensorMap* m, uint64_t* bar, int c0, in
 // A block works on up to kSlots tiles at a time, in the order in which it drew them:
 //   loading warp      draws a tile, starts its copies, looks up what it holds               -> full, told
 //   mapping warps     the map of every token (backward: its p) and of every warp's tokens    -> mapped
-//   publishing warp   joins the warps' maps to the tile's, hands that to the other blocks    -> known
+//   publishing warp   joins the warps' maps to the tile's, hands that to the other blocks
+//                     (`cut`: or at once what the tile hands on)                             -> known
 //   joining warp      finds the state before the tile, hands on the one behind it            -> ready
 //   walking warps     wait for that state, write the results                                 -> empty
 // So a tile whose state is late holds up nothing that another tile waits for: its map is out, and so are
@@ -494,6 +517,8 @@ struct ScanShared {
   uint64_t full[kSlots], told[kSlots], mapped[kSlots], known[kSlots], ready[kSlots], empty[kSlots];
   int tile[kSlots], slab[kSlots], info[kSlots];
   int dist[kSlots];                                // maps between the tile and the state that it starts from
+  int cut[kSlots];                                 // the break that decides what the tile hands on, -1: see scan_load
+  int handed[kSlots];                              // the publishing warp has handed it on
   int abort_flag;
   int reset[kSlots][kScanWarps];
   // Per warp and channel the map of its tokens; in a tile without breaks the publishing warp puts that of all
@@ -559,15 +584,27 @@ template <bool FWD, int TENSORS>
 DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&tm)[TENSORS], const ScanWork& w,
                     int tiles, int slabs, int slab_ch, bool joins, const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
-  auto draw = [&] { return atomicAdd(reinterpret_cast<unsigned long long*>(w.ctl), 1ull); };
-  unsigned long long next = lane == 0 ? draw() : 0;
+  unsigned long long turn = 0;
+  int slab = 0, k = 0, mine = 0, edge = 0;
+  // draws the next tile and looks up what it and its neighbours hold, ahead of the slot that it will take
+  auto draw = [&] {
+    unsigned long long ticket = 0;
+    if (lane == 0) ticket = atomicAdd(reinterpret_cast<unsigned long long*>(w.ctl), 1ull);
+    ticket = __shfl_sync(0xffffffffu, ticket, 0);
+    // tile by tile, its slabs side by side
+    turn = ticket >> 32 ? ticket / (unsigned)slabs : (uint32_t)ticket / (uint32_t)slabs;
+    if (turn >= (unsigned)tiles) return;
+    slab = static_cast<int>(ticket - turn * (unsigned)slabs);
+    k = FWD ? static_cast<int>(turn) : tiles - 1 - static_cast<int>(turn);
+    const int n = FWD ? k - lane : k + lane;
+    mine = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
+    edge = w.edge[k];
+  };
+  draw();
   int i = 0, ends = 0;
   for (;; ++i) {
     const int s = i % kSlots;
     if (i >= kSlots && !wait_phase(&sh.empty[s], ((i / kSlots) - 1) & 1, wc)) break;
-    const unsigned long long ticket = __shfl_sync(0xffffffffu, next, 0);
-    // tile by tile, its slabs side by side
-    const unsigned long long turn = ticket >> 32 ? ticket / (unsigned)slabs : (uint32_t)ticket / (uint32_t)slabs;
     if (turn >= (unsigned)tiles) {                   // the end, for all that take tiles in turn
       if (lane == 0) {
         sh.tile[s] = -1;
@@ -577,35 +614,35 @@ DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&t
       if (++ends == kSlots) break;
       continue;
     }
-    const int slab = static_cast<int>(ticket - turn * (unsigned)slabs);
-    const int k = FWD ? static_cast<int>(turn) : tiles - 1 - static_cast<int>(turn);
-    if (lane == 0) {
-      sh.tile[s] = k;
-      sh.slab[s] = slab;
-      mbar_expect_tx(&sh.full[s], TENSORS * kPlane);
-#pragma unroll
-      for (int a = 0; a < TENSORS; ++a)
-        tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * kTile);
-    }
-    // what the tile holds, and what the tiles before it (backward: behind it) do
     const int n = FWD ? k - lane : k + lane;
-    int info = (lane <= kScanGroup && n >= 0 && n < tiles) ? w.info[n] : kInfoBreak;
+    int info = mine;
     // the mapping warps' maps hold: no break in the tile, and backward nothing that joins at a node's end
     const bool mapped = !(info & kInfoBreak) && (FWD || !(info & kInfoSource || (joins && (info & kInfoEnd))));
     const bool map = mapped && (FWD ? (n + 1) % kScanGroup != 0 : (info & kInfoOut) && n % kScanGroup != 0);
     const uint32_t run = __ballot_sync(0xffffffffu, map);
     info = __shfl_sync(0xffffffffu, info | (mapped ? kInfoMapped : 0) | (map ? kInfoMap : 0), 0);
-    if (lane == 0) {
+    // The tile's last break (backward: the first) where what the tile hands on is a plain map of what that break
+    // starts from (is known from the tokens before it): it is handed on before the tile is walked, whose turn comes
+    // after those of the block's earlier tiles (32768 x 2048 rollout: 210 -> 142 us forward, 342 -> 326 backward).
+    const bool cut = FWD ? info & kInfoLast : (info & kInfoFirst) && !(joins && (info & kInfoFirstEnd));
+    if (lane == 0) {                                 // (all of it there for those who wait for `full`, too)
+      sh.tile[s] = k;
+      sh.slab[s] = slab;
       sh.info[s] = info;
+      sh.cut[s] = !cut ? -1 : FWD ? edge >> 8 : edge & 255;
       sh.dist[s] = __ffs(~(run >> 1)) - 1;
       mbar_arrive(&sh.told[s]);
+      mbar_expect_tx(&sh.full[s], TENSORS * kPlane);
+#pragma unroll
+      for (int a = 0; a < TENSORS; ++a)
+        tma_load_2d(slots + (size_t)(s * kPlanes + a) * kPlane, tm[a], &sh.full[s], slab * slab_ch, k * kTile);
     }
     // The first tiles are drawn one at a time, so that neighbours go to different blocks; later ones ahead.
     if (i + 1 < kSlots && !wait_phase(&sh.full[s], 0, wc)) {
       ++i;
       break;
     }
-    if (lane == 0) next = draw();
+    draw();
   }
   // every copy has landed before the block's shared memory goes, also where other warps gave up
   // (slots that hold an end had their copies used before)
@@ -630,7 +667,7 @@ DEVI bool next_tile(const ScanShared& sh, uint64_t (&bar)[kSlots], int i, Tile& 
   if (!wait_phase(&bar[t.s], t.parity, wc)) return false;
   t.k = sh.tile[t.s];
   t.slab = sh.slab[t.s];
-  t.info = sh.info[t.s];                             // (valid from `told` on)
+  t.info = sh.info[t.s];
   return t.k >= 0;
 }
 DEVI void warp_arrive(uint64_t* bar) {
@@ -666,6 +703,12 @@ struct Rows {
     word(0, i) = a.v[0];
     word(1, i) = b.v[0];
     if constexpr (CH == 2) *reinterpret_cast<float2*>(pair + i * 2 * kRow) = make_float2(a.v[1], b.v[1]);
+  }
+  DEVI Vec<CH> decay(int i) const {
+    Vec<CH> a;
+    a.v[0] = word(0, i);
+    if constexpr (CH == 2) a.v[1] = *reinterpret_cast<const float*>(pair + i * 2 * kRow);
+    return a;
   }
   DEVI Vec<CH> step(int i, Vec<CH> h) const {        // a h + b
     Vec<CH> a, b;
@@ -723,13 +766,28 @@ struct Joiner {
   }
 };
 
+// The state that the break at token j starts from, in v.  Not null: where it is polled (it is another tile's to write)
+template <typename T, int CH>
+DEVI const float* cut_row(const ScanFwd<T>& a, int j, int ch, Vec<CH>& v) {
+  const int n = a.w.link[j];
+  const bool on = ch < a.C;
+  const float* row = a.states + (size_t)max(n, 0) * a.C + ch;
+  v = vec<CH>(0.f);
+  if (n >= 0 && on) v = look_state(row, v);
+  if (n < 0 && a.init) v = ld_state_if(a.init + (size_t)a.t.tok_node[j] * a.C + ch, on, v);
+  return n >= 0 && on ? row : nullptr;
+}
+
 // The publishing warp.  It waits for no other block, so that a tile's map is out as soon as it can be.
-template <int CH>
-DEVI void fwd_publish(ScanShared& sh, const ScanWork& w, int C, int slab_ch, const WaitCtl& wc) {
-  const int lane = threadIdx.x & 31;
+template <typename T>
+DEVI void fwd_publish(const ScanFwd<T>& a, ScanShared& sh, int slab_ch, const WaitCtl& wc) {
+  constexpr int CH = Lane<T>::CH;
+  const ScanWork& w = a.w;
+  const int lane = threadIdx.x & 31, C = a.C;
   Tile t;
   for (int i = 0; next_tile(sh, sh.told, i, t, wc); ++i) {
     if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+    const int ch = t.slab * slab_ch + lane * CH, cut = sh.cut[t.s];
     if (t.info & kInfoMapped) {
       Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
 #pragma unroll 8
@@ -740,8 +798,22 @@ DEVI void fwd_publish(ScanShared& sh, const ScanWork& w, int C, int slab_ch, con
         B = vfma(qa, B, qb);
         A = A * qa;
       }
-      const int ch = t.slab * slab_ch + lane * CH;
       if ((t.info & kInfoMap) && ch < C) hand_map(w.maps + ((size_t)t.k * C + ch) * 2, A, B);
+      sh_st(sh.all[t.s][0], A);
+      sh_st(sh.all[t.s][1], B);
+    } else if (cut >= 0) {
+      Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f);
+      for (int q = cut / kWarpTokens; q < kScanWarps; ++q) {
+        const Vec<CH> qa = sh_ld<CH>(sh.A[t.s][q]);
+        B = vfma(qa, B, sh_ld<CH>(sh.B[t.s][q]));
+        A = A * qa;
+      }
+      // handed on here if the state is there already, else by the joining warp
+      Vec<CH> v;
+      const float* row = cut_row(a, t.k * kTile + cut, ch, v);
+      const bool there = __all_sync(0xffffffffu, !row || is_full(v));
+      if (there && ch < C) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * C + ch, vfma(A, v, B));
+      if (lane == 0) sh.handed[t.s] = there;
       sh_st(sh.all[t.s][0], A);
       sh_st(sh.all[t.s][1], B);
     }
@@ -778,6 +850,10 @@ DEVI void bwd_publish(ScanShared& sh, ScanBack& back, const ScanWork& w, const f
       if ((t.info & kInfoMap) && ch < C) hand_map(w.maps + ((size_t)t.k * C + ch) * 2, A, R);
       sh_st(sh.all[t.s][0], A);
       sh_st(sh.all[t.s][1], R);
+    } else if (sh.cut[t.s] >= 0) {
+      Vec<CH> R = vec<CH>(0.f);
+      for (int q = sh.cut[t.s] / kWarpTokens; q >= 0; --q) R = vfma(sh_ld<CH>(sh.A[t.s][q]), R, sh_ld<CH>(back.R[t.s][q]));
+      if (ch < C) hand_state(w.carry + (size_t)t.k * C + ch, R);
     }
     warp_arrive(&sh.known[t.s]);
   }
@@ -787,8 +863,8 @@ DEVI void bwd_publish(ScanShared& sh, ScanBack& back, const ScanWork& w, const f
 // state behind the nearest tile before it that is no plain map or ends a group of kScanGroup; backward the same
 // from the other side.  Groups bound the maps that a tile joins; within one, no tile waits for a state to be
 // handed on.  rows: the states between tiles (backward: the gradients).
-template <bool FWD, int CH>
-DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, float* rows, int slab_ch, int joiner,
+template <bool FWD, int CH, typename Late>
+DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, float* rows, int slab_ch, int joiner, const Late& late,
                     const WaitCtl& wc) {
   const int lane = threadIdx.x & 31;
   Tile t;
@@ -798,6 +874,19 @@ DEVI void scan_join(ScanShared& sh, const ScanWork& w, int C, float* rows, int s
     const int b = FWD ? t.k - 1 - dist : t.k + 1 + dist;
     const Joiner<CH> j{w, C, ch, b, FWD ? 1 : -1, dist, rows + (size_t)(need ? b : 0) * C + ch, on};
     Vec<CH> v = vec<CH>(0.f);
+    if (FWD && sh.cut[t.s] >= 0) {
+      if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
+      if (!sh.handed[t.s]) {                           // what the publishing warp did not wait for
+        bool ok = true;
+        if constexpr (FWD) ok = late(t.k * kTile + sh.cut[t.s], ch, v);
+        if (!ok) {
+          if (lane == 0) sh.abort_flag = 1;
+          return;
+        }
+        if (on) hand_state(rows + (size_t)t.k * C + ch, vfma(sh_ld<CH>(sh.all[t.s][0]), v, sh_ld<CH>(sh.all[t.s][1])));
+      }
+      v = vec<CH>(0.f);
+    }
     if (need && !j.join(v, wc)) {
       if (lane == 0) sh.abort_flag = 1;
       return;
@@ -826,6 +915,17 @@ DEVI void fwd_map(ScanShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
       rows.set_token(q, a, b);
       B = vfma(a, B, b);
       A = A * a;
+    }
+    const int cut = sh.cut[t.s] - warp * kWarpTokens;
+    if ((unsigned)cut < (unsigned)kWarpTokens) {       // (rare: the map once more, from there)
+      A = vec<CH>(1.f);
+      B = vec<CH>(0.f);
+#pragma unroll 1
+      for (int q = cut; q < kWarpTokens; ++q) {
+        const Vec<CH> a = rows.decay(q);
+        B = rows.step(q, B);
+        A = A * a;
+      }
     }
     sh_st(sh.A[t.s][warp], A);
     sh_st(sh.B[t.s][warp], B);
@@ -1023,7 +1123,7 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
     Vec<CH> last = vec<CH>(0.f);                       // the state behind the warp
     bool last_known = false;
     if (t.info & kInfoBreak) {
-      if (!wait_phase(&sh.mapped[t.s], t.parity, wc)) return;
+      if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
       if (serial) {                                    // no warp is a tile ahead, where its turn would overtake this one's
         warp_arrive(&g.own);
         if (!wait_phase(&g.own, n_own & 1, wc)) return;
@@ -1051,7 +1151,7 @@ DEVI void fwd_walk(const ScanFwd<T>& a, ScanShared& sh, ScanWalk& g, ScanEnds& k
         sh_st(g.carry[warp], v);
         warp_arrive(&g.turn[warp + 1]);
       }
-      if (warp == kScanWarps - 1 && f.on) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
+      if (warp == kScanWarps - 1 && f.on && sh.cut[t.s] < 0) hand_state(a.states + (size_t)(a.t.n_nodes + t.k) * a.C + ch, v);
     };
     if (last_known) hand_on(last);
     Vec<CH> h = vec<CH>(0.f);
@@ -1100,6 +1200,8 @@ DEVI void bwd_map(ScanShared& sh, ScanBack& back, uint8_t* slots, int warp, cons
   Tile t;
   for (int i = 0; next_tile(sh, sh.full, i, t, wc); ++i) {
     const Rows<T> rows(slots, t.s, warp);
+    int cut = sh.cut[t.s] - warp * kWarpTokens;        // what the warp hands on comes from the tokens before it
+    if ((unsigned)cut >= (unsigned)kWarpTokens) cut = kWarpTokens;
     Vec<CH> A = vec<CH>(1.f), B = vec<CH>(0.f), R = vec<CH>(0.f);
 #pragma unroll 4
     for (int q = 0; q < kWarpTokens; ++q) {
@@ -1107,8 +1209,10 @@ DEVI void bwd_map(ScanShared& sh, ScanBack& back, uint8_t* slots, int warp, cons
       rows.set_p(q, p);
       B = advance<KIND>(p, rows.get(1, q), B);
       // the gradient's map, from the first token on: u before = R + A u behind
-      R = vfma(decayed(p, A), rows.get(2, q), R);
-      A = decayed(p, A);
+      if (q < cut) {
+        A = decayed(p, A);
+        R = vfma(A, rows.get(2, q), R);
+      }
     }
     sh_st(sh.A[t.s][warp], A);
     sh_st(sh.B[t.s][warp], B);
@@ -1213,7 +1317,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
     // the four tokens in which the warp's first break lies: up to there h depends on what comes into the warp
     const int known = f.breaks ? (__ffs(f.breaks) - 1) & ~3 : kWarpTokens - 4;
     const bool near = __any_sync(0xffffffffu, f.kid_at >= 0);         // a node of this tile joins in the warp
-    if (!wait_phase(mapped ? &sh.known[t.s] : &sh.mapped[t.s], t.parity, wc)) return;
+    if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
     bool ok = true;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
@@ -1266,7 +1370,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
         sh_st(gr.carry[warp], v);
         warp_arrive(&gr.turn[warp - 1]);
       }
-      if (warp == 0 && on) hand_state(a.w.carry + (size_t)t.k * a.C + ch, v);
+      if (warp == 0 && on && sh.cut[t.s] < 0) hand_state(a.w.carry + (size_t)t.k * a.C + ch, v);
     };
     if (f.breaks && !near) hand_on(sh_ld<CH>(back.R[t.s][warp]));
     if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
@@ -1429,10 +1533,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_fwd(const __grid_const
     const CUtensorMap* tm[2] = {&tm_gate, &tm_x};
     scan_load<true>(sh, slots, tm, a.w, a.t.n_tiles, a.slabs, SLAB, false, wc);
   } else if (warp == LOAD + 1) {
-    fwd_publish<CH>(sh, a.w, a.C, SLAB, wc);
+    fwd_publish(a, sh, SLAB, wc);
   } else {
+    auto late = [&](int j, int ch, Vec<CH>& v) {
+      const float* row = cut_row(a, j, ch, v);
+      return __all_sync(0xffffffffu, arrived(row, v, row != nullptr, wc, a.w.ctl + 2)) != 0;
+    };
     scan_join<true, CH>(sh, a.w, a.C, a.states + (size_t)a.t.n_nodes * a.C, SLAB,
-                                   warp - LOAD - 2, wc);
+                                   warp - LOAD - 2, late, wc);
   }
 }
 
@@ -1462,7 +1570,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_bwd(const __grid_const
     bwd_publish<CH>(sh, back, a.w, a.states + (size_t)a.t.n_nodes * a.C, a.C, SLAB, wc);
   } else {
     scan_join<false, CH>(sh, a.w, a.C, a.w.carry, SLAB,
-                                    warp - LOAD - 2, wc);
+                                    warp - LOAD - 2, 0, wc);
   }
 }
 
@@ -1596,7 +1704,7 @@ int scan_slabs(int C, int dtype) {
 }
 
 struct ScanLayout {
-  size_t link, end, kid, sib, info, ctl, maps, dnode, carry, total;
+  size_t link, end, kid, sib, info, edge, ctl, maps, dnode, carry, total;
 };
 
 ScanLayout scan_layout(const tree_plan_t* p, int C) {
@@ -1608,6 +1716,7 @@ ScanLayout scan_layout(const tree_plan_t* p, int C) {
   L.kid = o;   o += tok;
   L.sib = o;   o += tok;
   L.info = o;  o = align256(o + tiles * 4);
+  L.edge = o;  o = align256(o + tiles * 4);
   L.ctl = o;   o = align256(o + 16);
   L.maps = o;  o = align256(o + tiles * C * 8);
   L.dnode = o; o = align256(o + (size_t)p->n_nodes * C * 4);
@@ -1620,7 +1729,7 @@ ScanWork scan_work(void* workspace, const ScanLayout& L) {
   uint8_t* w = static_cast<uint8_t*>(workspace);
   auto i32 = [&](size_t o) { return reinterpret_cast<int32_t*>(w + o); };
   auto f32 = [&](size_t o) { return reinterpret_cast<float*>(w + o); };
-  return ScanWork{i32(L.link), i32(L.end), i32(L.kid), i32(L.sib), i32(L.info), i32(L.ctl),
+  return ScanWork{i32(L.link), i32(L.end), i32(L.kid), i32(L.sib), i32(L.info), i32(L.edge), i32(L.ctl),
                   f32(L.maps), f32(L.dnode), f32(L.carry)};
 }
 
