@@ -390,7 +390,9 @@ size_t tree_scan_workspace(const tree_plan_t* plan, int C);
  * other path.
  * C a multiple of 8 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
  * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at
- * a time.  Deterministic.  status_dev (device int32, may be NULL) as for tree_attn_fwd. */
+ * a time.  y may be gate or x itself; otherwise no output (the workspace among them) overlaps another
+ * buffer (else TREE_ERR_ARG): states of the step before are read from rows of their own.
+ * Deterministic.  status_dev (device int32, may be NULL) as for tree_attn_fwd. */
 int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len,
                   const void* gate, const void* x, const float* init, int C, int dtype,
                   int gate_kind, void* workspace, void* y, float* states, int32_t* status_dev,
@@ -401,7 +403,8 @@ int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t*
  * gate, x, init, states: the forward's.  Writes dgate, dx [N][C] (type dtype) and, if d_init is not
  * NULL, the gradient of init (fp32 [n_nodes][C], zeros in rows that the forward does not read).
  * h is computed again from states.  Deterministic: a node's state collects its children's gradients
- * from the last child to the first.  Rules as tree_scan_fwd. */
+ * from the last child to the first.  Rules as tree_scan_fwd; dgate and dx may each be one of gate, x
+ * and dy itself. */
 int tree_scan_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len,
                   const void* gate, const void* x, const float* init, const float* states,
                   const void* dy, const float* d_final, int C, int dtype, int gate_kind,

@@ -356,3 +356,25 @@ def test_offsets_beyond_32_bits():
     for name, got in (("y", y), ("dgate", dg), ("dx", dx)):
         _close(name, got[:, idx], ref[name], ref["e_" + name], torch.bfloat16)
     _close("final", st[:1, idx], ref["final"], ref["e_final"], torch.float32)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n_nodes,max_len", [(20, 6), (50, 60)])
+def test_outputs_in_the_place_of_inputs(dtype, n_nodes, max_len):
+    """y in x, then dgate in gate and dx in dy, as a whole: the same bits as in buffers of their own."""
+    parent, node_len = random_tree(480 + n_nodes, n_nodes, max_len=max_len, n_roots=2)
+    N, C = int(node_len.sum()), 200
+    gate, x, init, dy, dfin = (t.to(DEV) for t in _inputs(N, n_nodes, C, "sigmoid", dtype, 18))
+    plan, tree = tam.tree_plan(parent, node_len, device=DEV), tam.tree_arrays(parent, node_len, DEV)
+    y, st = tam.tree_scan_fwd(plan, tree, gate, x, init=init)
+    dg, dx, di = tam.tree_scan_bwd(plan, tree, gate, x, st, dy, init=init, d_final=dfin)
+    for keep in (x.clone(), gate.clone()):
+        other = gate if torch.equal(keep, x) else x
+        y2, st2 = (tam.tree_scan_fwd(plan, tree, other, keep, init=init, y=keep) if other is gate
+                   else tam.tree_scan_fwd(plan, tree, keep, other, init=init, y=keep))
+        assert torch.equal(y, y2) and torch.equal(st, st2)
+    g2, d2 = gate.clone(), dy.clone()
+    _, _, di2 = tam.tree_scan_bwd(plan, tree, g2, x, st, d2, init=init, d_final=dfin, dgate=g2, dx=d2)
+    assert torch.equal(dg, g2) and torch.equal(dx, d2) and torch.equal(di, di2)
+    with pytest.raises(tam.TreeError):
+        tam.tree_scan_fwd(plan, tree, gate, x, init=st[:n_nodes], states=st)

@@ -62,6 +62,36 @@ def test_scan(lib, plan):
     assert lib.tree_scan_workspace(ctypes.byref(plan), 64) > 0
 
 
+def test_scan_buffers_that_overlap(lib, plan):
+    """Outputs overlap nothing but a per-token input as a whole (that is let through to the check of the device)."""
+    M = 1 << 22
+    names = ("parent", "node_len", "gate", "x", "init", "ws", "y", "states", "dy", "dfin", "dg", "dx", "di")
+    at = {n: A + i * M for i, n in enumerate(names)}
+    tokens, nodes = 160 * 64 * 2, 2 * 64 * 4
+
+    def fwd(**kw):
+        a = {**at, **kw}
+        return lib.tree_scan_fwd(ctypes.byref(plan), a["parent"], a["node_len"], a["gate"], a["x"], a["init"], 64, 0, 0,
+                                 a["ws"], a["y"], a["states"], None, None)
+
+    def bwd(**kw):
+        a = {**at, **kw}
+        return lib.tree_scan_bwd(ctypes.byref(plan), a["parent"], a["node_len"], a["gate"], a["x"], a["init"], a["states"],
+                                 a["dy"], a["dfin"], 64, 0, 0, a["ws"], a["dg"], a["dx"], a["di"], None, None)
+
+    for name in ("gate", "x", "init", "y"):
+        size = nodes if name == "init" else tokens
+        for off in (0, 16, size - 16):
+            assert fwd(states=at[name] + off) == ARG and fwd(ws=at[name] + off) == ARG
+    assert fwd(init=at["states"]) == ARG and fwd(y=at["x"] + 16) == ARG and fwd(y=at["gate"] + tokens - 16) == ARG
+    for name in ("gate", "x", "dy", "init", "dfin", "states", "dg", "dx"):
+        assert bwd(di=at[name]) == ARG and bwd(ws=at[name]) == ARG, name
+    assert bwd(dg=at["dx"]) == ARG and bwd(dx=at["dy"] + 16) == ARG and bwd(dg=at["states"]) == ARG
+    if not torch.cuda.is_available():                  # what is allowed gets as far as the device, of which there is none
+        for call in (fwd(), fwd(y=at["x"]), fwd(y=at["gate"]), bwd(), bwd(dx=at["dy"]), bwd(dg=at["gate"], dx=at["x"])):
+            assert call not in (0, ARG, SHAPE)
+
+
 def test_rope_axes(lib, plan):
     def call(fn, sections=(16, 24, 24), inter=0, n=None, pos=A, q=A, Hq=4, Hkv=2, d=128, theta=1e4):
         s = (ctypes.c_int32 * max(1, len(sections)))(*sections)

@@ -1745,6 +1745,27 @@ int scan_args(const tree_plan_t* plan, const int32_t* parent, const int32_t* nod
   return TREE_OK;
 }
 
+// A call's buffers.  An output overlaps nothing, but that a per-token output may be a per-token input as a whole:
+// a tile's inputs are in shared memory before its outputs are written, and no other tile reads them.
+struct Buffer {
+  const void* p;
+  size_t bytes;
+  bool tokens;
+};
+bool buffers_ok(const Buffer* out, int n_out, const Buffer* in, int n_in) {
+  auto meet = [](const Buffer& a, const Buffer& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
+  };
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (meet(out[i], in[j]) && !(out[i].tokens && in[j].tokens && out[i].p == in[j].p)) return false;
+  }
+  return true;
+}
+
 ScanTree scan_tree(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len) {
   return ScanTree{plan->tok_node, plan->tok_start, plan->sub_end, parent, node_len,
                   plan->n_tokens, plan->n_nodes,   scan_tiles(plan)};
@@ -1869,6 +1890,11 @@ int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t*
   for (const void* p : {gate, x, (const void*)workspace, (const void*)y, (const void*)states})
     if (!p || misaligned(p)) return TREE_ERR_ARG;
   if (init && misaligned(init)) return TREE_ERR_ARG;
+  const size_t tokens = (size_t)plan->n_tokens * C * (dtype == TREE_BF16 ? 2 : 4), nodes = (size_t)plan->n_nodes * C * 4;
+  const Buffer out[] = {{workspace, scan_layout(plan, C).total, false}, {y, tokens, true},
+                        {states, (size_t)tree_scan_rows(plan) * C * 4, false}};
+  const Buffer in[] = {{gate, tokens, true}, {x, tokens, true}, {init, nodes, false}};
+  if (!buffers_ok(out, 3, in, 3)) return TREE_ERR_ARG;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1889,6 +1915,12 @@ int tree_scan_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_t*
     if (!p || misaligned(p)) return TREE_ERR_ARG;
   for (const void* p : {(const void*)init, (const void*)d_final, (const void*)d_init})
     if (p && misaligned(p)) return TREE_ERR_ARG;
+  const size_t tokens = (size_t)plan->n_tokens * C * (dtype == TREE_BF16 ? 2 : 4), nodes = (size_t)plan->n_nodes * C * 4;
+  const Buffer out[] = {{workspace, scan_layout(plan, C).total, false}, {dgate, tokens, true}, {dx, tokens, true},
+                        {d_init, nodes, false}};
+  const Buffer in[] = {{gate, tokens, true}, {x, tokens, true}, {dy, tokens, true}, {init, nodes, false},
+                       {d_final, nodes, false}, {states, (size_t)tree_scan_rows(plan) * C * 4, false}};
+  if (!buffers_ok(out, 4, in, 6)) return TREE_ERR_ARG;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
