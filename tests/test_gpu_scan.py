@@ -378,3 +378,23 @@ def test_outputs_in_the_place_of_inputs(dtype, n_nodes, max_len):
     assert torch.equal(dg, g2) and torch.equal(dx, d2) and torch.equal(di, di2)
     with pytest.raises(tam.TreeError):
         tam.tree_scan_fwd(plan, tree, gate, x, init=st[:n_nodes], states=st)
+
+
+@pytest.mark.parametrize("kind,dtype", [("sigmoid", torch.float32), ("log", torch.bfloat16)])
+@pytest.mark.parametrize("parent,lens", [
+    ([-1, 0, 0, 2], [100, 60, 40, 56]),                # 256 tokens, a path across the tile's edge
+    ([-1, 0], [128, 128]), ([-1, -1], [128, 100]),     # it goes on there, and it does not
+    ([-1] * 200, [1] * 200), ([-1, 0, 1, 0], [127, 0, 1, 1]),
+    ([-1] + [0] * 99, [30] + [1] * 99)], ids=range(6))
+def test_two_tiles_of_tokens(kind, dtype, parent, lens):
+    """The states row between the two, which the backward starts from."""
+    check(parent, lens, 72, kind, dtype, 21, ends=len(lens) % 2 == 0)
+
+
+@pytest.mark.parametrize("kind,dtype", [("sigmoid", torch.bfloat16), ("log", torch.float32)])
+@pytest.mark.parametrize("lens", [[1] * 700, [0, 2] * 200, [0] * 450 + [150, 300] + [1] * 200, [1] * 127 + [0] * 400 + [300]],
+                         ids=range(4))
+def test_a_step_of_many_sequences(kind, dtype, lens):
+    """Nodes that are sequences of their own, no more tokens than nodes: most have one token, some go across tiles."""
+    assert 256 < sum(lens) <= len(lens)
+    check([-1] * len(lens), lens, 136, kind, dtype, 22, ends=len(lens) != 700 or kind == "log")

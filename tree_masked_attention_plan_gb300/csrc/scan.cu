@@ -1574,41 +1574,51 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_bwd(const __grid_const
   }
 }
 
-// Forward for at most a tile of tokens (a decoding step): one launch, a block a slab, no maps and nothing to
-// wait for.  Latency is all: the gates and inputs of a warp's eight tokens are on their way while lanes 0-7
-// find out where these start from; then each warp walks the trees that begin within its eight tokens to
-// their ends.  By 4096 bf16 channels: 64 one-token nodes in 4.6 us (20.6 by the kernels for many tokens), 128 in
-// 5.5 (22), a chain of 128 in 6.3 (10.4), a chain of 64 with 64 one-token children in 14 (52).
-constexpr int kStepWarps = 16, kStepTokens = kTile / kStepWarps;
+// Forward for a step of decoding: one launch, no maps and nothing to wait for.  A block takes a slab and up to
+// kStepMost tokens.  Either these are all there are, of whatever tree; or every node is a sequence of its own,
+// hardly of more than a token, and the block walks those that begin in it.  Latency is all: the gates and inputs of a warp's
+// eight tokens are on their way while lanes 0-7 find out where these start from; then each warp walks the trees
+// that begin within its eight tokens to their ends.  By 4096 bf16 channels, in us (by the kernels for many tokens):
+// 64 one-token nodes 4.6 (20.6), 300 6.7 (27), 4096 57 (104); a chain of 256 11.2 (11.3), one of 128 with 128
+// one-token children 26 (28).
+constexpr int kStepTokens = 8, kStepMost = 2 * kTile;  // a warp's tokens; a block's (1024 threads)
 template <typename T>
-constexpr int step_smem(int N) { return (N + kStepTokens - 1) / kStepTokens * kStepTokens * 2 * 32 * Lane<T>::CH * 4; }
+constexpr int step_smem(int n) { return (n + kStepTokens - 1) / kStepTokens * kStepTokens * 2 * 32 * Lane<T>::CH * 4; }
 
 template <typename T, int KIND>
-__global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, const T* x, const ScanFwd<T> a) {
+__global__ void __launch_bounds__(32 * kStepMost / kStepTokens) k_scan_step(const T* gate, const T* x, int span, const ScanFwd<T> a) {
   constexpr int CH = Lane<T>::CH, SLAB = kRow / (int)sizeof(T);
   extern __shared__ float step_rows[];                 // per token: its decays, its inputs (its states once walked)
-  __shared__ int from[kTile], node[kTile];             // where a break's state lies, the token's node
-  __shared__ uint32_t bits[kStepWarps][3];             // per warp's tokens: roots' first, breaks, nodes' last
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.t.N;
+  __shared__ int from[kStepMost], node[kStepMost];     // where a break's state lies, the token's node
+  __shared__ uint32_t bits[kStepMost / kStepTokens][3];             // per warp's tokens: roots' first, breaks, nodes' last
+  const int base = blockIdx.y * span, n = min(span, a.t.N - base);  // the block's tokens: counted from base below
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ch = blockIdx.x * SLAB + lane * CH, t0 = warp * kStepTokens, j = t0 + lane;
   const bool on = ch < a.C;
-  auto decay = [&](int j) { return step_rows + j * 2 * 32 * CH; };
-  auto input = [&](int j) { return step_rows + (j * 2 + 1) * 32 * CH; };
+  auto decay = [&](int q) { return step_rows + q * 2 * 32 * CH; };
+  auto input = [&](int q) { return step_rows + (q * 2 + 1) * 32 * CH; };
+  auto word = [&](const T* p, int q) { return __ldg(reinterpret_cast<const uint32_t*>(p + (size_t)(base + q) * a.C + ch)); };
+  // behind token q, h the state there: kept between tiles; nothing goes on from the last token's tile, whose row holds
+  // no leftovers
+  auto between = [&](int q, Vec<CH> h) {
+    const int t = base + q + 1;
+    if (on && t == a.t.N) st_state(a.states + (size_t)(a.t.n_nodes + (t - 1) / kTile) * a.C + ch, t % kTile ? vec<CH>(0.f) : h);
+    else if (on && t % kTile == 0) st_state(a.states + (size_t)(a.t.n_nodes + (t - 1) / kTile) * a.C + ch, h);
+  };
   uint32_t gw[kStepTokens], xw[kStepTokens];
 #pragma unroll
   for (int q = 0; q < kStepTokens; ++q) {
-    const size_t at = (size_t)(t0 + q) * a.C + ch;
-    const bool in = on && t0 + q < N;
-    gw[q] = in ? __ldg(reinterpret_cast<const uint32_t*>(gate + at)) : 0u;
-    xw[q] = in ? __ldg(reinterpret_cast<const uint32_t*>(x + at)) : 0u;
+    const bool in = on && t0 + q < n;
+    gw[q] = in ? word(gate, t0 + q) : 0u;
+    xw[q] = in ? word(x, t0 + q) : 0u;
   }
   int start = kLinkChain, own = 0;
   bool last = false;
-  if (lane < kStepTokens && j < N) {
-    own = a.t.tok_node[j];
-    const int first = a.t.tok_start[own], len = a.t.node_len[own];
+  if (lane < kStepTokens && j < n) {
+    own = a.t.tok_node[base + j];
+    const int first = a.t.tok_start[own] - base, len = a.t.node_len[own];
     const int up = j == first ? scan_token_ancestor(own, a.t) : -1;
-    const int src = up < 0 ? -1 : a.t.tok_start[up] + a.t.node_len[up] - 1;
+    const int src = up < 0 ? -1 : a.t.tok_start[up] + a.t.node_len[up] - 1 - base;
     if (j == first) start = src < 0 || src >= j ? kLinkRoot : src == j - 1 ? kLinkChain : up;
     last = j == first + len - 1;
     from[j] = src;
@@ -1630,7 +1640,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
   }
 #pragma unroll
   for (int q = 0; q < kStepTokens; ++q) {
-    if (t0 + q >= N) break;
+    if (t0 + q >= n) break;
     Vec<CH> d, b;
     token_of<KIND>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
     if ((roots >> q) & 1u) b = vfma(d, h0[q], b);
@@ -1638,7 +1648,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
     sh_st(input(t0 + q), b);
   }
   // rows of nodes without tokens
-  for (int v0 = warp * 32; v0 < a.t.n_nodes; v0 += kStepWarps * 32) {
+  for (int v0 = blockIdx.y * blockDim.x + warp * 32; v0 < a.t.n_nodes; v0 += gridDim.y * blockDim.x) {
     const int v = v0 + lane;
     uint32_t m = __ballot_sync(0xffffffffu, v < a.t.n_nodes && a.t.node_len[min(v, a.t.n_nodes - 1)] <= 0);
     for (; m; m &= m - 1)
@@ -1649,9 +1659,9 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
   Vec<CH> h = vec<CH>(0.f);
   int q0 = __ffs(roots) - 1;
 #pragma unroll 1
-  for (int w = warp; w * kStepTokens < N; ++w, q0 = 0) {
+  for (int w = warp; w * kStepTokens < n; ++w, q0 = 0) {
     const uint32_t rt = bits[w][0], br = bits[w][1], en = bits[w][2];
-    const int at = w * kStepTokens, q1 = min(w > warp && rt ? __ffs(rt) - 1 : kStepTokens, N - at);
+    const int at = w * kStepTokens, q1 = min(w > warp && rt ? __ffs(rt) - 1 : kStepTokens, n - at);
     Vec<CH> d[kStepTokens], b[kStepTokens];
     int src[kStepTokens];
 #pragma unroll
@@ -1660,8 +1670,8 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
       b[q] = sh_ld<CH>(input(at + q));
       src[q] = from[at + q];
     }
-    T* y = a.y + (size_t)at * a.C + ch;
-    if (!br && q1 == kStepTokens) {                    // (no branch between the tokens: a chain of 128 by 4096 in 6.3 us, else 13.3)
+    T* y = a.y + (size_t)(base + at) * a.C + ch;
+    if (!br && q1 == kStepTokens) {                    // (no branch between the tokens: a chain of 128 by 4096 in 6.9 us, else 13.3)
 #pragma unroll
       for (int q = 0; q < kStepTokens; ++q, y += a.C) {
         h = vfma(d[q], h, b[q]);
@@ -1685,9 +1695,30 @@ __global__ void __launch_bounds__(32 * kStepWarps) k_scan_step(const T* gate, co
       if (on) st_state(a.states + (size_t)node[q] * a.C + ch, sh_ld<CH>(input(q)));
     }
     if (w > warp && rt) return;
+    between(min(at + kStepTokens, n) - 1, h);
   }
-  // the row behind the tile, which nothing here goes on from, holds no leftovers
-  if (on) st_state(a.states + (size_t)a.t.n_nodes * a.C + ch, N == kTile ? h : vec<CH>(0.f));
+  // a sequence that goes on behind the block's tokens (only where every node is a sequence of its own)
+  if (base + n >= a.t.N) return;
+  const int v = node[n - 1], end = min(a.t.tok_start[v] + a.t.node_len[v], a.t.N) - base;
+#pragma unroll 1
+  for (int at = n; at < end; at += kStepTokens) {
+#pragma unroll
+    for (int q = 0; q < kStepTokens; ++q) {
+      const bool in = on && at + q < end;
+      gw[q] = in ? word(gate, at + q) : 0u;
+      xw[q] = in ? word(x, at + q) : 0u;
+    }
+#pragma unroll
+    for (int q = 0; q < kStepTokens; ++q) {
+      if (at + q >= end) break;
+      Vec<CH> d, b;
+      token_of<KIND>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
+      h = vfma(d, h, b);
+      if (on) *reinterpret_cast<uint32_t*>(a.y + (size_t)(base + at + q) * a.C + ch) = Lane<T>::pack(h);
+      if (on && at + q == end - 1) st_state(a.states + (size_t)v * a.C + ch, h);
+      between(at + q, h);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -1807,11 +1838,15 @@ int scan_grid(int64_t units, unsigned* blocks) {
 // 12 bytes a channel are marked empty for each tile: a block for 1024 channels
 dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (unsigned)((C + 1023) / 1024)); }
 
+// `span` tokens a block
 template <typename T, int KIND>
-int run_step(const ScanFwd<T>& a, const void* gate, const void* x, cudaStream_t s) {
-  int rc = announce<&k_scan_step<T, KIND>, step_smem<T>(kTile)>();
+int run_step(const ScanFwd<T>& a, const void* gate, const void* x, int span, cudaStream_t s) {
+  const int rc = announce<&k_scan_step<T, KIND>, step_smem<T>(kStepMost)>();
   if (rc) return rc;
-  k_scan_step<T, KIND><<<a.slabs, 32 * kStepWarps, step_smem<T>(a.t.N), s>>>(static_cast<const T*>(gate), static_cast<const T*>(x), a);
+  const int n = std::min(span, a.t.N), warps = (n + kStepTokens - 1) / kStepTokens;
+  const dim3 grid((unsigned)a.slabs, (unsigned)((a.t.N + span - 1) / span));
+  k_scan_step<T, KIND><<<grid, 32 * warps, step_smem<T>(n), s>>>(static_cast<const T*>(gate),
+                                                                 static_cast<const T*>(x), span, a);
   return record_cuda(cudaGetLastError());
 }
 template <typename T, int KIND>
@@ -1832,13 +1867,17 @@ int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, c
 }
 
 template <typename T>
-int scan_fwd(const ScanTree& t, const ScanWork& w, const void* gate, const void* x, const float* init, int C, int dtype,
+int scan_fwd(const ScanTree& t, int paths, const ScanWork& w, const void* gate, const void* x, const float* init, int C, int dtype,
              int kind, void* y, float* states, int32_t* status, cudaStream_t s) {
   const int slabs = scan_slabs(C, dtype);
   const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
-  if (t.N <= kTile)
-    return kind == TREE_GATE_SIGMOID ? run_step<T, TREE_GATE_SIGMOID>(a, gate, x, s)
-                                     : run_step<T, TREE_GATE_LOG>(a, gate, x, s);
+  // Few tokens, or (as many paths as nodes: every node is a sequence of its own) a token a sequence.
+  const bool step = paths == t.n_nodes && t.N <= t.n_nodes && t.N <= 65535 * kTile;
+  if (step || t.N <= kStepMost) {
+    const int span = step ? kTile : kStepMost;         // (more blocks where they can be)
+    return kind == TREE_GATE_SIGMOID ? run_step<T, TREE_GATE_SIGMOID>(a, gate, x, span, s)
+                                     : run_step<T, TREE_GATE_LOG>(a, gate, x, span, s);
+  }
   CUtensorMap tg, tx;
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
@@ -1901,8 +1940,8 @@ int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t*
   const ScanTree t = scan_tree(plan, parent, node_len);
   const ScanWork w = scan_work(workspace, scan_layout(plan, C));
   return dtype == TREE_BF16
-             ? scan_fwd<__nv_bfloat16>(t, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s)
-             : scan_fwd<float>(t, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s);
+             ? scan_fwd<__nv_bfloat16>(t, plan->n_paths, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s)
+             : scan_fwd<float>(t, plan->n_paths, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s);
 }
 
 int tree_scan_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len, const void* gate,
