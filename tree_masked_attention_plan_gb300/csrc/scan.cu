@@ -387,6 +387,12 @@ DEVI Vec<1> ld_state_if(const float* p, bool want, Vec<1>) {
                : "=&f"(r.v[0]) : "l"(p), "r"((uint32_t)want) : "memory");
   return r;
 }
+// the same through L1, of what no block of the kernel writes
+DEVI Vec<2> ld_given_if(const float* p, bool want, Vec<2>) {
+  const float2 a = want ? __ldg(reinterpret_cast<const float2*>(p)) : make_float2(0.f, 0.f);
+  return {{a.x, a.y}};
+}
+DEVI Vec<1> ld_given_if(const float* p, bool want, Vec<1>) { return {{want ? __ldg(p) : 0.f}}; }
 DEVI void st_state(float* p, Vec<2> v) { __stcg(reinterpret_cast<float2*>(p), make_float2(v.v[0], v.v[1])); }
 DEVI void st_state(float* p, Vec<1> v) { __stcg(p, v.v[0]); }
 // Values that other blocks wait for: a lane's state, and its map h -> A h + B as (A, B) per channel.  Each
@@ -1222,59 +1228,49 @@ DEVI void bwd_map(ScanShared& sh, ScanBack& back, uint8_t* slots, int warp, cons
   }
 }
 
-// Backward, a warp at whose 16 tokens paths break or join.
+// Backward, a warp at whose 16 tokens paths break or join.  One token at a time, in rolled loops: it is rare, and
+// straight-line code for four tokens (some 10 KB) was fetched anew each time, which took longer than the steps.
 template <typename T, int KIND>
 struct BwdBreaks {
   static constexpr int CH = Lane<T>::CH;
   const ScanBwd<T>& a;
   const Rows<T>& rows;
-  int t0, tok0, ch;                        // tok0: t0's place in the tile
+  int t0, ch;
   bool on;
   int from, end, kid, sib, own;            // per lane q < 16, of token t0 + q; own: its node
   uint32_t breaks, joins;
   int kid_at, sib_at;                      // per lane: the token of this tile at which kid, sib starts; -1: in another
-  // h before four tokens from g on; h: before token g, and on return behind the four
-  DEVI void befores(int g, Vec<CH>& h, Vec<CH> (&b)[4]) const {
-    if ((breaks >> g) & 15u) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = __shfl_sync(0xffffffffu, from, g + q), v = __shfl_sync(0xffffffffu, own, g + q);
-        const bool brk = (breaks >> (g + q)) & 1u;
-        const float* row = n >= 0 ? a.states + (size_t)n * a.C : (a.init && brk ? a.init + (size_t)v * a.C : nullptr);
-        b[q] = ld_state_if(row + ch, on && row && brk, h);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if (!((breaks >> (g + q)) & 1u)) b[q] = h;
-      h = advance<KIND>(rows.p(g + q), rows.get(1, g + q), b[q]);
-    }
+  // the state that the break at token q starts from
+  DEVI Vec<CH> start_of(int q) const {
+    const int n = __shfl_sync(0xffffffffu, from, q), v = __shfl_sync(0xffffffffu, own, q);
+    const float* row = n >= 0 ? a.states + (size_t)n * a.C : (a.init ? a.init + (size_t)v * a.C : nullptr);
+    return ld_given_if(row + ch, on && row, Vec<CH>());
   }
-  // the kid of token q, -1 where there is none or it starts in these very four tokens
-  DEVI int kid_behind(int q) const {
-    const int kd = __shfl_sync(0xffffffffu, kid, q), at = __shfl_sync(0xffffffffu, kid_at, q);
-    return at >= 0 && (tok0 + q) / 4 == at / 4 ? -1 : kd;
+  // h before token q, from h before token g; held: the state that the break at token `at` starts from
+  DEVI Vec<CH> before(int g, int q, Vec<CH> h, int& at, Vec<CH>& held) const {
+    const uint32_t m = breaks & ((2u << q) - 1u) & ~((1u << g) - 1u);
+    int r = g;
+    if (m) {
+      r = 31 - __clz(m);
+      if (r != at) held = start_of(r);
+      at = r;
+      h = held;
+    }
+#pragma unroll 1
+    for (; r < q; ++r) h = advance<KIND>(rows.p(r), rows.get(1, r), h);
+    return h;
   }
-  // dy of four tokens and what joins it: kid: the next node that starts from this one's state, with those behind
-  // it; end: the node's own final state.  False if a wait gave up.
-  DEVI bool sums(int g, Vec<CH> (&d)[4], const WaitCtl& wc) const {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) d[q] = rows.get(2, g + q);
-    if (!((joins >> g) & 15u)) return true;
-    Vec<CH> f[4], k[4];
-    bool ok = true;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int kd = kid_behind(g + q), e = __shfl_sync(0xffffffffu, end, g + q);
-      f[q] = ld_state_if(a.d_final + (size_t)e * a.C + ch, on && a.d_final && e >= 0, d[q]);
-      k[q] = ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on && kd >= 0, d[q]);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int kd = kid_behind(g + q);
-      ok = arrived(a.w.dnode + (size_t)kd * a.C + ch, k[q], on && kd >= 0, wc, a.w.ctl + 2) && ok;
-      d[q] = d[q] + (f[q] + k[q]);
-    }
+  // dy of token q and what joins it: kid: the next node that starts from this one's state, with those behind it;
+  // end: the node's own final state.  False if a wait gave up.
+  DEVI bool sum(int q, Vec<CH>& d, const WaitCtl& wc) const {
+    d = rows.get(2, q);
+    if (!((joins >> q) & 1u)) return true;
+    const int kd = __shfl_sync(0xffffffffu, kid, q), e = __shfl_sync(0xffffffffu, end, q);
+    const float* row = a.w.dnode + (size_t)kd * a.C + ch;
+    const Vec<CH> f = ld_state_if(a.d_final + (size_t)e * a.C + ch, on && a.d_final && e >= 0, d);
+    Vec<CH> k = ld_state_if(row, on && kd >= 0, d);
+    const bool ok = arrived(row, k, on && kd >= 0, wc, a.w.ctl + 2);
+    d = d + (f + k);
     return __all_sync(0xffffffffu, ok);
   }
 };
@@ -1293,7 +1289,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
     const int ch = t.slab * SLAB + lane * CH;
     const int t0 = t.k * kTile + warp * kWarpTokens;
     const bool mapped = t.info & kInfoMapped, serial = t.info & kInfoSerialBack;
-    BwdBreaks<T, KIND> f{a, rows, t0, warp * kWarpTokens, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u, -1, -1};
+    BwdBreaks<T, KIND> f{a, rows, t0, ch, ch < a.C, kLinkChain, -1, -1, -1, -1, 0u, 0u, -1, -1};
     n_turn += serial;
     const bool on = f.on;
     Vec<CH> h = vec<CH>(0.f);
@@ -1314,31 +1310,30 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
       f.joins = __ballot_sync(0xffffffffu, f.kid >= 0 || (f.end >= 0 && a.d_final));
     }
     const uint32_t special = f.breaks | f.joins;
-    // the four tokens in which the warp's first break lies: up to there h depends on what comes into the warp
-    const int known = f.breaks ? (__ffs(f.breaks) - 1) & ~3 : kWarpTokens - 4;
-    const bool near = __any_sync(0xffffffffu, f.kid_at >= 0);         // a node of this tile joins in the warp
+    // Up to the four tokens in which the warp's first break lies h depends on what comes into the warp, and what the
+    // warp hands on depends on the tokens before that break only; in some of these (`late`) a node of this tile joins.
+    const int first = f.breaks ? __ffs(f.breaks) - 1 : kWarpTokens, known = min(first, kWarpTokens - 1) & ~3;
+    const uint32_t kids = __ballot_sync(0xffffffffu, f.kid_at >= 0);
+    const bool late = kids & ((1u << first) - 1u);
     if (!wait_phase(&sh.known[t.s], t.parity, wc)) return;
     bool ok = true;
     if (!mapped) {
       if (f.breaks) {                                  // h behind the warp does not depend on h before it
-        Vec<CH> v = vec<CH>(0.f), b[4];
+        Vec<CH> v = vec<CH>(0.f);
 #pragma unroll 1
-        for (int g = known; g < kWarpTokens; g += 4) {
-          sh_st(back.before[warp][g / 4], v);
-          f.befores(g, v, b);
+        for (int q = first; q < kWarpTokens; ++q) {
+          if (q > first && q % 4 == 0) sh_st(back.before[warp][q / 4], v);
+          if ((f.breaks >> q) & 1u) v = f.start_of(q);
+          v = advance<KIND>(rows.p(q), rows.get(1, q), v);
         }
         sh_st(sh.B[t.s][warp], v);
       }
-      if (special && !near) {                          // what the warp hands on depends on its tokens up to there
-        Vec<CH> R = vec<CH>(0.f), d[4];
+      if (special && !late) {
+        Vec<CH> R = vec<CH>(0.f), d;
 #pragma unroll 1
-        for (int g = known; g >= 0; g -= 4) {
-          ok = f.sums(g, d, wc) && ok;
-#pragma unroll
-          for (int q = 3; q >= 0; --q) {
-            R = decayed(rows.p(g + q), d[q] + R);
-            if ((f.breaks >> (g + q)) & 1u) R = vec<CH>(0.f);
-          }
+        for (int q = first - 1; q >= 0; --q) {
+          ok = f.sum(q, d, wc) && ok;
+          R = decayed(rows.p(q), d + R);
         }
         sh_st(back.R[t.s][warp], R);
       }
@@ -1372,7 +1367,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
       }
       if (warp == 0 && on && sh.cut[t.s] < 0) hand_state(a.w.carry + (size_t)t.k * a.C + ch, v);
     };
-    if (f.breaks && !near) hand_on(sh_ld<CH>(back.R[t.s][warp]));
+    if (f.breaks && !late) hand_on(sh_ld<CH>(back.R[t.s][warp]));
     if (!wait_phase(&sh.ready[t.s], t.parity, wc)) return;
     Vec<CH> u = sh_ld<CH>(sh.in[t.s]);
     if (mapped) {
@@ -1387,7 +1382,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
       u = sh_ld<CH>(gr.carry[warp + 1]);
     }
     // a warp in which nothing of this tile joins hands on by its map, before it walks
-    if (!mapped && !f.breaks && !near) hand_on(vfma(sh_ld<CH>(sh.A[t.s][warp]), u, sh_ld<CH>(back.R[t.s][warp])));
+    if (!mapped && !f.breaks && !late) hand_on(vfma(sh_ld<CH>(sh.A[t.s][warp]), u, sh_ld<CH>(back.R[t.s][warp])));
     auto wait_row = [&](int tok) {                     // of a node that starts in this tile
       const bool there = wait_until([&] { return *(volatile int*)&gr.row_of[tok] == n_turn; }, wc, a.w.ctl + 2);
       ok = __all_sync(0xffffffffu, there) && ok;
@@ -1443,37 +1438,27 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
 #pragma unroll
         for (int q = 3; q >= 0; --q) step(g + q, rows.get(2, g + q) + u, b[q]);
       } else {
-        Vec<CH> d[4];
-        f.befores(g, h, b);
-        for (uint32_t m = near ? (f.joins >> g) & 15u : 0u; m; m &= m - 1) {
-          const int at = __shfl_sync(0xffffffffu, f.kid_at, g + __ffs(m) - 1);
-          if (at >= 0 && at / 4 != (f.tok0 + g) / 4) wait_row(at);                  // (those of these four: below)
-        }
-        ok = f.sums(g, d, wc) && ok;
-#pragma unroll
-        for (int q = 3; q >= 0; --q) {
-          const int kd = __shfl_sync(0xffffffffu, f.kid, g + q);
-          // a node that starts within these four tokens hands its gradient on only now
-          if (kd >= 0 && __any_sync(0xffffffffu, f.from != kLinkChain && f.own == kd && lane < kWarpTokens)) {
-            const Vec<CH> again = ld_state_if(a.w.dnode + (size_t)kd * a.C + ch, on, u);
-            const int e = __shfl_sync(0xffffffffu, f.end, g + q);
-            const Vec<CH> own = ld_state_if(a.d_final + (size_t)e * a.C + ch, on && a.d_final && e >= 0, u);
-            d[q] = rows.get(2, g + q) + (own + again);
-          }
-          step(g + q, d[q] + u, b[q]);
-          if ((f.breaks >> (g + q)) & 1u) {            // what this path hands to the state it started from
-            const int n = __shfl_sync(0xffffffffu, f.from, g + q), v = __shfl_sync(0xffffffffu, f.own, g + q);
-            const int sb = __shfl_sync(0xffffffffu, f.sib, g + q);
-            const int sb_at = __shfl_sync(0xffffffffu, f.sib_at, g + q);
-            if (sb_at >= 0) wait_row(sb_at);
-            const float* row = a.w.dnode + (size_t)sb * a.C + ch;
-            Vec<CH> later = ld_state_if(row, on && sb >= 0, u);
-            ok = __all_sync(0xffffffffu, arrived(row, later, on && sb >= 0, wc, a.w.ctl + 2)) && ok;
-            if (on && n >= 0) hand_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
-            if (on && n == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
-            u = vec<CH>(0.f);
-            if (serial) row_written(gr, warp * kWarpTokens + g + q, n_turn);
-          }
+        int held_at = -1;
+        Vec<CH> held = h;
+#pragma unroll 1
+        for (int q = g + 3; q >= g; --q) {
+          const int kid_at = __shfl_sync(0xffffffffu, f.kid_at, q);
+          if (kid_at >= 0) wait_row(kid_at);
+          Vec<CH> d;
+          ok = f.sum(q, d, wc) && ok;
+          step(q, d + u, f.before(g, q, h, held_at, held));
+          if (!((f.breaks >> q) & 1u)) continue;
+          // what this path hands to the state it started from
+          const int n = __shfl_sync(0xffffffffu, f.from, q), v = __shfl_sync(0xffffffffu, f.own, q);
+          const int sb = __shfl_sync(0xffffffffu, f.sib, q), sib_at = __shfl_sync(0xffffffffu, f.sib_at, q);
+          if (sib_at >= 0) wait_row(sib_at);
+          const float* row = a.w.dnode + (size_t)sb * a.C + ch;
+          Vec<CH> later = ld_state_if(row, on && sb >= 0, u);
+          ok = __all_sync(0xffffffffu, arrived(row, later, on && sb >= 0, wc, a.w.ctl + 2)) && ok;
+          if (on && n >= 0) hand_state(a.w.dnode + (size_t)v * a.C + ch, u + later);
+          if (on && n == kLinkRoot && a.d_init) st_state(a.d_init + (size_t)v * a.C + ch, u);
+          u = vec<CH>(0.f);
+          if (serial) row_written(gr, warp * kWarpTokens + q, n_turn);
         }
       }
     }
@@ -1481,7 +1466,7 @@ DEVI void bwd_walk(const ScanBwd<T>& a, ScanShared& sh, ScanBack& back, ScanWalk
       if (lane == 0) sh.abort_flag = 1;
       return;
     }
-    if (near) hand_on(u);
+    if (late) hand_on(u);
     warp_arrive(&sh.empty[t.s]);
   }
 }
