@@ -122,7 +122,7 @@ DEVI bool is_source(int v, const ScanTree& t) {
   return next < t.sub_end[v] && t.sub_end[t.tok_node[next]] < t.sub_end[v];
 }
 
-// Blocks (tile, share of the channels): links and info; the tile's map and the state behind it marked empty.  FWD:
+// Blocks (tile, 0): links and info.  Blocks (tile, share of the channels from 1 on): the tile's map and the state behind it marked empty.  FWD:
 // states of nodes that breaks start from marked empty, of nodes without tokens zeroed.  Backward: dnode of nodes
 // that start at a break from another's state marked empty, d_init of those that do not start from it zeroed.
 template <bool FWD>
@@ -130,9 +130,9 @@ __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, 
   __shared__ int bits, lo, hi;
   __shared__ uint8_t marks[kTile];
   const int k = blockIdx.x, j = k * kTile + threadIdx.x;
-  {
+  if (blockIdx.y) {
     const uint4 e = make_uint4(kEmpty, kEmpty, kEmpty, kEmpty);
-    const int first = blockIdx.y * kTile + threadIdx.x, step = gridDim.y * kTile;
+    const int first = (blockIdx.y - 1) * kTile + threadIdx.x, step = (gridDim.y - 1) * kTile;
     uint4* m = reinterpret_cast<uint4*>(w.maps + (size_t)k * C * 2);
     uint4* b = reinterpret_cast<uint4*>(between + (size_t)k * C);
     for (int i = first; i < C / 2; i += step) m[i] = e;
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(kTile) k_scan_prepare(ScanTree t, ScanWork w, 
       }
       __syncthreads();
     }
+    return;
   }
-  if (blockIdx.y) return;
   if (threadIdx.x == 0) {
     bits = 0;
     lo = kTile;
@@ -1820,8 +1820,8 @@ int scan_grid(int64_t units, unsigned* blocks) {
   return rc;
 }
 
-// 12 bytes a channel are marked empty for each tile: a block for 1024 channels
-dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, (unsigned)((C + 1023) / 1024)); }
+// 12 bytes a channel are marked empty for each tile: a block for 1024 channels; and one for the links
+dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, 1u + (unsigned)((C + 1023) / 1024)); }
 
 // `span` tokens a block
 template <typename T, int KIND>
