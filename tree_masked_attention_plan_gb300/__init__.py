@@ -248,7 +248,9 @@ def tree_plan(parent, node_len, device=None, stream=None, pos_offset=0) -> TreeP
     lib = _lib()
     info = PlanInfo()
     _check(lib.tree_plan_query(par.ctypes.data, nl.ctypes.data, len(par), ctypes.byref(info)), "tree_plan_query")
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+    dev = torch.device("cuda" if device is None else device)
+    if dev.type == "cuda" and dev.index is None:      # the current device, by its number, as tensors name it
+        dev = torch.device("cuda", torch.cuda.current_device())
     buf = torch.empty(int(info.plan_bytes), dtype=torch.uint8, device=dev)
     c = PlanT()
     _check(lib.tree_plan_bind(ctypes.byref(info), _ptr(buf), ctypes.byref(c)), "tree_plan_bind")
