@@ -758,18 +758,28 @@ def tree_scan_bwd(plan: TreePlan, tree, gate, x, states, dy, init=None, d_final=
 @dataclass
 class GradList:
     """A step's gradients gathered for tree_grad_norm and tree_grad_clip (tree_grad_list): the tensors, where
-    clipping writes them, the C list and a workspace.  The tensors' contents are read at every call."""
+    clipping writes them, the C list, and a workspace with the raw stream that it belongs to (None: a call takes
+    one of its own).  The tensors' contents are read at every call."""
     grads: list
     out: list
     c: ctypes.Array
     workspace: torch.Tensor
     device: torch.device
+    stream: int = None
 
 
 def tree_grad_list(grads, out=None) -> GradList:
     """Gather contiguous CUDA tensors (bf16 or fp32, any shapes, one device).  out: tensors of the same shapes
     and types that tree_grad_clip writes; None clips in place.  Gather once and use at every step, for as
-    long as the gradients stay in the same tensors; one call at a time (it holds the workspace)."""
+    long as the gradients stay in the same tensors; one call at a time (it holds the workspace, which belongs, like any
+    tensor, to the stream that is current here: a call on another stream comes after a wait for this one)."""
+    gl = _gather(grads, out)
+    gl.workspace = _grad_workspace(gl)
+    gl.stream = torch._C._cuda_getCurrentRawStream(gl.device.index)
+    return gl
+
+
+def _gather(grads, out=None) -> GradList:
     grads = list(grads)
     outs = grads if out is None else list(out)
     if not grads:
@@ -787,18 +797,26 @@ def tree_grad_list(grads, out=None) -> GradList:
         if o is not g:
             _need_on(dev, o, tuple(g.shape), g.dtype, f"out[{i}]")
         c[i] = GradT(g.data_ptr(), o.data_ptr(), g.numel(), _DTYPES[g.dtype], 0)
-    ws = torch.empty(int(_lib().tree_grad_workspace(len(grads))), dtype=torch.uint8, device=dev)
-    return GradList(grads=grads, out=outs, c=c, workspace=ws, device=dev)
+    return GradList(grads=grads, out=outs, c=c, workspace=None, device=dev)
+
+
+def _grad_workspace(gl):
+    return torch.empty(int(_lib().tree_grad_workspace(len(gl.grads))), dtype=torch.uint8, device=gl.device)
 
 
 def _grad_call(name, grads, norm, stream, *args):
-    gl = grads if isinstance(grads, GradList) else tree_grad_list(grads)
+    gl = grads if isinstance(grads, GradList) else _gather(grads)
     if norm is not None:
         _need_on(gl.device, norm, (1,), torch.float32, "norm")
 
     def call(st):
         out = torch.empty(1, dtype=torch.float32, device=gl.device) if norm is None else norm
-        _check(getattr(_lib(), name)(gl.c, len(gl.grads), *args, gl.workspace.data_ptr(), out.data_ptr(), st), name)
+        ws = gl.workspace
+        if ws is None:
+            ws = _grad_workspace(gl)                  # of the stream that the kernels run on
+        elif st != gl.stream:                         # not to be handed out again before they have ended
+            ws.record_stream(torch.cuda.current_stream(gl.device))
+        _check(getattr(_lib(), name)(gl.c, len(gl.grads), *args, ws.data_ptr(), out.data_ptr(), st), name)
         return out
 
     return _launch(gl.device, stream, call)
