@@ -70,6 +70,8 @@ typedef struct {
   int64_t plan_bytes; /* device bytes tree_plan_bind() carves the plan arrays from (the
                          arrays below plus 12 T bytes of per-tile counts tree_plan uses
                          as scratch, placed after `counts`) */
+  int32_t max_len;    /* the longest node's tokens */
+  int32_t reserved;   /* 0 */
 } tree_plan_info;
 
 /* Host-side descriptor of a plan; every pointer is device memory inside the buffer given
@@ -110,6 +112,7 @@ typedef struct {
   int32_t* tile_nruns;    /* [T] number of runs in the tile (may exceed TREE_MAX_RUNS) */
   int32_t* counts;        /* [4] nnz, n_full, n_partial, reserved (0) */
   int32_t n_nodes, n_tokens, n_tiles, n_paths;
+  int32_t max_len;        /* the longest node's tokens (tree_scan_fwd chooses by it; no result depends on it) */
 } tree_plan_t;
 
 /* Validate the tree and report its sizes.  Host only, no CUDA call.

@@ -1,9 +1,12 @@
 """Calls of the recurrence, the several-axis rotation and the gradient norm that their documentation allows, beside the
-ordinary ones: plans of a device without a number, lists that are dropped while another stream works on them."""
+ordinary ones: plans of a device without a number, lists that are dropped while another stream works on them, steps of
+sequences one of which is long."""
+import numpy as np
 import pytest
 import torch
 
 import tree_masked_attention_plan_gb300 as tam
+from oracle import scan as osc
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -60,3 +63,35 @@ def test_a_gradient_list_that_is_dropped_while_another_stream_works_on_it(held):
         torch.cuda.synchronize()
         assert torch.equal(norm, want)
     assert ((flat.double() - before.double() / 3).abs() <= 2.0 ** -20 * before.abs()).all()
+
+
+def _forward(lens, C=64, seed=3):
+    """Nodes that are sequences of their own through the recurrence, against its oracle (24 units of 2^-24 a token, as the
+    recurrence's own tests count them); whether it left the workspace as it was."""
+    N, n = sum(lens), len(lens)
+    g = torch.Generator().manual_seed(seed)
+    gate, x, init = torch.randn(N, C, generator=g) + 2, torch.randn(N, C, generator=g), torch.randn(n, C, generator=g)
+    plan, tree = tam.tree_plan([-1] * n, lens, device=DEV), tam.tree_arrays([-1] * n, lens, DEV)
+    ws = torch.full((tam.tree_scan_workspace(plan, C),), 0xA5, dtype=torch.uint8, device=DEV)
+    y, st = tam.tree_scan_fwd(plan, tree, gate.to(DEV), x.to(DEV), init=init.to(DEV), workspace=ws)
+    ref = osc.scan([-1] * n, lens, gate.double().numpy(), x.double().numpy(), "sigmoid", init=init.double().numpy())
+    for got, name in ((y, "y"), (st[:n], "final")):
+        err = np.abs(got.double().cpu().numpy() - ref[name])
+        assert (err <= 24 * 2.0 ** -24 * ref["e_" + name] + 2.0 ** -24 * np.abs(ref[name]) + 1e-37).all()
+    return bool((ws == 0xA5).all())
+
+
+@pytest.mark.parametrize("lens", [[0] * 3000 + [20000] + [0] * 17000, [1] * 700 + [0] * 5000 + [4000, 3] + [1] * 200])
+def test_one_long_sequence_among_many_empty_ones(lens):
+    """No more tokens than nodes, yet one sequence of many: a matter for the kernels that work along a sequence in
+    parallel, which keep what its tiles hand on in the workspace."""
+    assert sum(lens) <= len(lens)
+    assert not _forward(lens)
+
+
+@pytest.mark.parametrize("lens", [[1] * 600 + [3, 0, 0, 0, 2], [1] * 100 + [0] * 400 + [128] + [1] * 90 + [100, 77],
+                                  [0] * 500 + [1, 128, 128, 2, 126, 1]])
+def test_a_step_with_some_sequences_of_more_tokens(lens):
+    """One launch and nothing in the workspace; sequences that go on behind the 128 tokens of a block."""
+    assert 256 < sum(lens) <= len(lens) and max(lens) <= 128
+    assert _forward(lens)

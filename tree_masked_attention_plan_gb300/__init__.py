@@ -56,7 +56,7 @@ class TreeError(RuntimeError):
 
 class PlanInfo(ctypes.Structure):
     _fields_ = [("n_nodes", _i32), ("n_tokens", _i32), ("n_tiles", _i32), ("n_paths", _i32),
-                ("max_nnz", _i64), ("plan_bytes", _i64)]
+                ("max_nnz", _i64), ("plan_bytes", _i64), ("max_len", _i32), ("reserved", _i32)]
 
 
 PLAN_PTR_FIELDS = ["order", "dfs_in", "dfs_out", "tok_start", "depth_off", "leaves", "dfs_tok_start", "sub_end",
@@ -67,7 +67,7 @@ PLAN_PTR_FIELDS = ["order", "dfs_in", "dfs_out", "tok_start", "depth_off", "leav
 
 class PlanT(ctypes.Structure):
     _fields_ = [(f, _vp) for f in PLAN_PTR_FIELDS] + [("n_nodes", _i32), ("n_tokens", _i32),
-                                                      ("n_tiles", _i32), ("n_paths", _i32)]
+                                                      ("n_tiles", _i32), ("n_paths", _i32), ("max_len", _i32)]
 
 
 class GradT(ctypes.Structure):

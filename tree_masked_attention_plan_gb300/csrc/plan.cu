@@ -1,6 +1,7 @@
 // tree_plan: the node pass on the host, then per-token expansion and the 128x128 tile table
 // on the device ("Tree Training 技术详解": section 3.2 DFS serialization, section 4.3 node DFS
 // intervals and ancestor block table, section 5 depth positions, section 6.2 path counts).
+#include <algorithm>
 #include <cstdlib>
 #include <cstring>
 #include <vector>
@@ -13,7 +14,7 @@ namespace {
 constexpr int64_t kInt32Max = 2147483647LL;
 
 struct NodePass {
-  int n = 0, N = 0, T = 0, K = 0;
+  int n = 0, N = 0, T = 0, K = 0, longest = 0;
   // per node, 8 arrays in the device order of the node block
   std::vector<int32_t> block;   // [8 * n]: order, dfs_in, dfs_out, tok_start, depth_off, leaves,
                                 //          dfs_tok_start, sub_end
@@ -87,6 +88,7 @@ int node_pass(const int32_t* parent, const int32_t* node_len, int32_t n, NodePas
     if (parent[r] == -1) K += leaves[r];
   if (K > kInt32Max) return TREE_ERR_INVALID_TREE;
   out->N = (int)total;
+  out->longest = *std::max_element(node_len, node_len + n);
   out->T = (int)((total + TILE - 1) / TILE);
   out->K = (int)K;
   return TREE_OK;
@@ -344,6 +346,8 @@ int tree_plan_query(const int32_t* parent, const int32_t* node_len, int32_t n_no
   info->n_paths = np.K;
   info->max_nnz = (int64_t)np.T * (np.T + 1) / 2;
   info->plan_bytes = (int64_t)layout(np.n, np.N, np.T).total;
+  info->max_len = np.longest;
+  info->reserved = 0;
   return TREE_OK;
 }
 
@@ -388,6 +392,7 @@ int tree_plan_bind(const tree_plan_info* info, void* buf, tree_plan_t* p) {
   p->tile_nruns = reinterpret_cast<int32_t*>(b + L.nruns);
   p->counts = reinterpret_cast<int32_t*>(b + L.cnt);
   p->n_nodes = n; p->n_tokens = N; p->n_tiles = T; p->n_paths = info->n_paths;
+  p->max_len = info->max_len;
   return TREE_OK;
 }
 

@@ -1561,12 +1561,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) k_scan_bwd(const __grid_const
 
 // Forward for a step of decoding: one launch, no maps and nothing to wait for.  A block takes a slab and up to
 // kStepMost tokens.  Either these are all there are, of whatever tree; or every node is a sequence of its own,
-// hardly of more than a token, and the block walks those that begin in it.  Latency is all: the gates and inputs of a warp's
+// most of one token and none of many, and the block walks those that begin in it.  Latency is all: the gates and inputs of a warp's
 // eight tokens are on their way while lanes 0-7 find out where these start from; then each warp walks the trees
 // that begin within its eight tokens to their ends.  By 4096 bf16 channels, in us (by the kernels for many tokens):
 // 64 one-token nodes 4.6 (20.6), 300 6.7 (27), 4096 57 (104); a chain of 256 11.2 (11.3), one of 128 with 128
-// one-token children 26 (28).
+// one-token children 26 (28).  A sequence among one-token nodes is walked by one warp a slab, behind its block's tokens
+// from memory: 300 nodes and one of 128 tokens 14 (26), of 192 21 (26), of 256 29 (26), of 4096 649 (53); 4096 nodes and
+// one of 128 53 (83), of 512 105 (84).  Above kStepLongest that is left to the others.
 constexpr int kStepTokens = 8, kStepMost = 2 * kTile;  // a warp's tokens; a block's (1024 threads)
+constexpr int kStepLongest = kTile;
 template <typename T>
 constexpr int step_smem(int n) { return (n + kStepTokens - 1) / kStepTokens * kStepTokens * 2 * 32 * Lane<T>::CH * 4; }
 
@@ -1852,12 +1855,13 @@ int run_bwd(const ScanBwd<T>& a, const CUtensorMap& tg, const CUtensorMap& tx, c
 }
 
 template <typename T>
-int scan_fwd(const ScanTree& t, int paths, const ScanWork& w, const void* gate, const void* x, const float* init, int C, int dtype,
+int scan_fwd(const ScanTree& t, int paths, int longest, const ScanWork& w, const void* gate, const void* x, const float* init, int C, int dtype,
              int kind, void* y, float* states, int32_t* status, cudaStream_t s) {
   const int slabs = scan_slabs(C, dtype);
   const ScanFwd<T> a{init, static_cast<T*>(y), states, t, w, C, slabs, status, wait_limit_ns()};
-  // Few tokens, or (as many paths as nodes: every node is a sequence of its own) a token a sequence.
-  const bool step = paths == t.n_nodes && t.N <= t.n_nodes && t.N <= 65535 * kTile;
+  // Few tokens, or a step: every node is a sequence of its own (as many paths as nodes), on average of at most a token
+  // and none longer than kStepLongest.
+  const bool step = paths == t.n_nodes && t.N <= t.n_nodes && longest <= kStepLongest && t.N <= 65535 * kTile;
   if (step || t.N <= kStepMost) {
     const int span = step ? kTile : kStepMost;         // (more blocks where they can be)
     return kind == TREE_GATE_SIGMOID ? run_step<T, TREE_GATE_SIGMOID>(a, gate, x, span, s)
@@ -1925,8 +1929,8 @@ int tree_scan_fwd(const tree_plan_t* plan, const int32_t* parent, const int32_t*
   const ScanTree t = scan_tree(plan, parent, node_len);
   const ScanWork w = scan_work(workspace, scan_layout(plan, C));
   return dtype == TREE_BF16
-             ? scan_fwd<__nv_bfloat16>(t, plan->n_paths, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s)
-             : scan_fwd<float>(t, plan->n_paths, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s);
+             ? scan_fwd<__nv_bfloat16>(t, plan->n_paths, plan->max_len, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s)
+             : scan_fwd<float>(t, plan->n_paths, plan->max_len, w, gate, x, init, C, dtype, gate_kind, y, states, status_dev, s);
 }
 
 int tree_scan_bwd(const tree_plan_t* plan, const int32_t* parent, const int32_t* node_len, const void* gate,
