@@ -1,6 +1,6 @@
 """Calls of the recurrence, the several-axis rotation and the gradient norm that their documentation allows, beside the
 ordinary ones: plans of a device without a number, lists that are dropped while another stream works on them, steps of
-sequences one of which is long."""
+sequences one of which is long, waits that run out."""
 import numpy as np
 import pytest
 import torch
@@ -95,3 +95,45 @@ def test_a_step_with_some_sequences_of_more_tokens(lens):
     """One launch and nothing in the workspace; sequences that go on behind the 128 tokens of a block."""
     assert 256 < sum(lens) <= len(lens) and max(lens) <= 128
     assert _forward(lens)
+
+
+def test_waits_that_run_out():
+    """A path through 469 tiles under the shortest limit: some of the tiles that are worked on at once wait longer than 0.1
+    ms for the state before them.  The status word says so, the call ends, and the next one with the same buffers is right."""
+    parent, lens, trunk = [-1], [256], 0
+    while sum(lens) < 60000:                           # a trunk's segment, the leaf that follows it, then the trunk's next
+        parent += [trunk, len(lens)]
+        lens += [64, 16]
+        trunk = len(lens) - 2
+    N, n, C = sum(lens), len(lens), 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    gate, x, dy = r(N, C) + 2, r(N, C), r(N, C)
+    plan, tree = tam.tree_plan(parent, lens, device=DEV), tam.tree_arrays(parent, lens, DEV)
+    ws = torch.empty(tam.tree_scan_workspace(plan, C), dtype=torch.uint8, device=DEV)
+    status = tam.new_status(DEV)
+
+    def forward():
+        return tam.tree_scan_fwd(plan, tree, gate, x, workspace=ws, status=status)
+
+    def backward(states):
+        return tam.tree_scan_bwd(plan, tree, gate, x, states, dy, workspace=ws, status=status)[:2]
+
+    want = forward()
+    want += backward(want[1])
+    tam.check_status(status, "scan")
+    for call in (forward, lambda: backward(want[1])):
+        tam.tree_set_wait_limit_ns(100000)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            tam.tree_set_wait_limit_ns(2000000000)
+        assert status.item() == -5
+        with pytest.raises(tam.TreeError):
+            tam.check_status(status, "scan")
+        status.zero_()
+        got = forward()
+        got += backward(got[1])
+        tam.check_status(status, "scan")
+        assert all(torch.equal(a, b) for a, b in zip(want, got))

@@ -462,6 +462,7 @@ DEVI void set_release(int32_t* p, int bits) {      // *p |= bits, after everythi
 // Wait for a phase of a barrier, the whole warp.  Most warps of a block wait most of the time, so a look at the
 // barrier sleeps for up to kNap ns before it says no; the limit is looked at between naps.
 constexpr uint32_t kNap = 20000;
+constexpr uint64_t kDrainNs = 2000000000;           // for a block's copies in flight (they land within microseconds)
 DEVI bool wait_phase(uint64_t* bar, uint32_t parity, const WaitCtl& wc) {
   uint64_t t0 = 0;
   for (;;) {
@@ -651,12 +652,12 @@ DEVI void scan_load(ScanShared& sh, uint8_t* slots, const CUtensorMap* const (&t
     draw();
   }
   // every copy has landed before the block's shared memory goes, also where other warps gave up
-  // (slots that hold an end had their copies used before)
+  // (slots that hold an end had their copies used before); the limit that a caller sets for waits does not shorten this one
   if (lane == 0)
     for (int q = max(0, i - kSlots); q < i; ++q) {
       const uint64_t t0 = global_timer_ns();
       while (sh.tile[q % kSlots] >= 0 && !mbar_try_wait(&sh.full[q % kSlots], (q / kSlots) & 1) &&
-             global_timer_ns() - t0 < wc.limit_ns) {
+             global_timer_ns() - t0 < max(wc.limit_ns, kDrainNs)) {
       }
     }
 }
