@@ -391,7 +391,7 @@ size_t tree_scan_workspace(const tree_plan_t* plan, int C);
  * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout; y is rounded
  * once.  A state that becomes infinite or NaN stays so (either) along its paths and touches no
  * other path.
- * C a multiple of 8 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
+ * C a multiple of 8, at most 2^28 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
  * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at
  * a time.  y may be gate or x itself; otherwise no output (the workspace among them) overlaps another
  * buffer (else TREE_ERR_ARG): states of the step before are read from rows of their own.

@@ -1,6 +1,7 @@
 """Calls of the recurrence, the several-axis rotation and the gradient norm that their documentation allows, beside the
 ordinary ones: plans of a device without a number, lists that are dropped while another stream works on them, steps of
-sequences one of which is long, waits that run out."""
+sequences one of which is long, waits that run out, very
+wide layers."""
 import numpy as np
 import pytest
 import torch
@@ -137,3 +138,31 @@ def test_waits_that_run_out():
         got += backward(got[1])
         tam.check_status(status, "scan")
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("lens", [[2], [1, 3, 2]])
+def test_a_layer_wider_than_a_grid_goes(lens):
+    """2^26 + 2^20 channels of a few tokens: more slabs and more shares of 1024 channels than 65535.  The sampled channels
+    hold their own values, the others zeros."""
+    N, n, C = sum(lens), len(lens), (1 << 26) + (1 << 20)
+    at = torch.tensor([0, 1, 63, 64, 1 << 20, (1 << 26) - 1, 1 << 26, C - 1], device=DEV)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    gate, x, dy = (torch.randn(N, 8, generator=g, device=DEV).to(B) for _ in range(3))
+
+    def wide(v):
+        w = torch.zeros(N, C, dtype=B, device=DEV)
+        w[:, at] = v
+        return w
+
+    parent = list(range(-1, n - 1))
+    plan, tree = tam.tree_plan(parent, lens, device=DEV), tam.tree_arrays(parent, lens, DEV)
+    status = tam.new_status(DEV)
+    narrow = tam.tree_scan_fwd(plan, tree, gate, x)
+    narrow += tam.tree_scan_bwd(plan, tree, gate, x, narrow[1], dy)[:2]
+    g, v, d = wide(gate), wide(x), wide(dy)
+    got = tam.tree_scan_fwd(plan, tree, g, v, status=status)
+    got += tam.tree_scan_bwd(plan, tree, g, v, got[1], d, status=status)[:2]
+    tam.check_status(status, "scan")
+    for i, (a, b) in enumerate(zip(got, narrow)):
+        assert torch.equal(a[:, at], b), i
+        assert int((a != 0).sum()) <= a.shape[0] * 8

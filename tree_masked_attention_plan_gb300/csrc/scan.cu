@@ -55,6 +55,8 @@ constexpr int kRow = 128;                   // bytes of a tile's row: 64 bf16 or
 constexpr int kPlane = kTile * kRow;         // one tensor's rows of a tile
 constexpr int kScanGroup = 4;               // at most this many maps are joined to a state (8: 131072 x 2048 2 % slower)
 
+constexpr int kMostChannels = 1 << 28;      // a row's bytes and the channels behind its last slab still count as int
+
 constexpr int kLinkChain = -1;             // the token before on the path is the one before in packed order
 constexpr int kLinkRoot = -2;              // the token starts from its node's initial state
 
@@ -1759,7 +1761,7 @@ int scan_args(const tree_plan_t* plan, const int32_t* parent, const int32_t* nod
   int rc = plan_ok(plan);
   if (rc) return rc;
   if (!plan->tok_node || !plan->tok_start || !plan->sub_end || !parent || !node_len) return TREE_ERR_ARG;
-  if (plan->n_nodes <= 0 || C <= 0 || C % 8 != 0) return TREE_ERR_SHAPE;
+  if (plan->n_nodes <= 0 || C <= 0 || C > kMostChannels || C % 8 != 0) return TREE_ERR_SHAPE;
   if ((dtype != TREE_BF16 && dtype != TREE_F32) || (kind != TREE_GATE_SIGMOID && kind != TREE_GATE_LOG))
     return TREE_ERR_SHAPE;
   return TREE_OK;
@@ -1824,8 +1826,13 @@ int scan_grid(int64_t units, unsigned* blocks) {
   return rc;
 }
 
-// 12 bytes a channel are marked empty for each tile: a block for 1024 channels; and one for the links
-dim3 prepare_grid(const ScanTree& t, int C) { return dim3((unsigned)t.n_tiles, 1u + (unsigned)((C + 1023) / 1024)); }
+// 12 bytes a channel are marked empty for each tile: a block for 1024 channels, as far as a grid goes; and one for the links
+template <bool FWD>
+int run_prepare(const ScanTree& t, const ScanWork& w, int C, float* rows, float* between, cudaStream_t s) {
+  const dim3 grid((unsigned)t.n_tiles, 1u + (unsigned)std::min((C + 1023) / 1024, 65534));
+  k_scan_prepare<FWD><<<grid, kTile, 0, s>>>(t, w, C, rows, between);
+  return record_cuda(cudaGetLastError());
+}
 
 // `span` tokens a block
 template <typename T, int KIND>
@@ -1872,7 +1879,8 @@ int scan_fwd(const ScanTree& t, int paths, int longest, const ScanWork& w, const
   int rc = scan_map<T>(&tg, gate, C, t.N);
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<true><<<prepare_grid(t, C), kTile, 0, s>>>(t, w, C, states, states + (size_t)t.n_nodes * C);
+  rc = run_prepare<true>(t, w, C, states, states + (size_t)t.n_nodes * C, s);
+  if (rc) return rc;                                 // (the next kernel trusts what this one left)
   return kind == TREE_GATE_SIGMOID ? run_fwd<T, TREE_GATE_SIGMOID>(a, tg, tx, s)
                                    : run_fwd<T, TREE_GATE_LOG>(a, tg, tx, s);
 }
@@ -1887,7 +1895,8 @@ int scan_bwd(const ScanTree& t, const ScanWork& w, const void* gate, const void*
   if (!rc) rc = scan_map<T>(&tx, x, C, t.N);
   if (!rc) rc = scan_map<T>(&td, dy, C, t.N);
   if (rc) return rc;
-  k_scan_prepare<false><<<prepare_grid(t, C), kTile, 0, s>>>(t, w, C, d_init, w.carry);
+  rc = run_prepare<false>(t, w, C, d_init, w.carry, s);
+  if (rc) return rc;
   const ScanBwd<T> a{init, states, d_final, static_cast<T*>(dgate), static_cast<T*>(dx), d_init, t, w, C, slabs, status,
                      wait_limit_ns()};
   return kind == TREE_GATE_SIGMOID ? run_bwd<T, TREE_GATE_SIGMOID>(a, tg, tx, td, s)
