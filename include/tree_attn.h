@@ -180,7 +180,8 @@ int tree_apply_weights(const tree_plan_t* plan, const tree_bf16* u, tree_bf16* d
  * [n_axes], sum d/2, each >= 0) say how many frequencies an axis has: interleaved = 0, the first
  * sections[0] are axis 0's, the next sections[1] axis 1's, and so on; interleaved = 1, axis i >= 1
  * has i, i + n_axes, i + 2 n_axes, ... until it has its share (all of them below d/2), and axis 0
- * what is left.  Rotate-half pairs and layouts as tree_rope_fwd; in place allowed.  The angle is
+ * what is left.  Rotate-half pairs and layouts as tree_rope_fwd; in place allowed (qr = q, kr = k),
+ * no other overlap of an output with another buffer (TREE_ERR_ARG).  The angle is
  * exact to 2^-24 turns at every position.  One axis with pos = the plan's `pos` is
  * tree_rope_fwd with more exact angles.  n_axes outside 1..TREE_MAX_AXES, sections that do not
  * describe d/2 frequencies, d not 64/128, bad heads or theta -> TREE_ERR_SHAPE. */

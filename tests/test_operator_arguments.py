@@ -4,6 +4,7 @@ import os
 
 import numpy as np
 import pytest
+import torch
 
 import tree_masked_attention_plan_gb300 as tam
 
@@ -36,3 +37,33 @@ def test_scan_of_more_channels_than_its_counts_hold(lib):
     for C in (2 ** 28 + 8, 2 ** 30, 2 ** 31 - 8):
         assert lib.tree_scan_fwd(ctypes.byref(plan), A, A, A, A, None, C, 0, 0, A, A, A, None, None) == SHAPE
         assert lib.tree_scan_bwd(ctypes.byref(plan), A, A, A, A, None, A, A, None, C, 0, 0, A, A, A, None, None, None) == SHAPE
+
+
+def test_rope_axes_buffers_that_overlap(lib):
+    """An output overlaps nothing but its own input as a whole (that is let through to the check of the device)."""
+    par, nl = np.array([-1, 0], np.int32), np.array([100, 60], np.int32)
+    info, plan = tam.PlanInfo(), tam.PlanT()
+    assert lib.tree_plan_query(par.ctypes.data, nl.ctypes.data, 2, ctypes.byref(info)) == 0
+    assert lib.tree_plan_bind(ctypes.byref(info), ctypes.c_void_p(1 << 20), ctypes.byref(plan)) == 0
+    N, Hq, Hkv, d, M = 160, 4, 2, 64, 1 << 24
+    size = dict(pos=N * 3 * 4, q=N * Hq * d * 2, k=N * Hkv * d * 2, qr=N * Hq * d * 2, kr=N * Hkv * d * 2)
+    at = {n: (1 << 30) + i * M for i, n in enumerate(size)}
+    sec = (ctypes.c_int32 * 3)(12, 10, 10)
+
+    for fn in (lib.tree_rope_axes_fwd, lib.tree_rope_axes_bwd):
+        def call(**kw):
+            a = {**at, **kw}
+            return fn(ctypes.byref(plan), a["pos"], sec, 3, 0, a["q"], a["k"], a["qr"], a["kr"], Hq, Hkv, d, 1e4, None)
+
+        for out, own in (("qr", "q"), ("kr", "k")):
+            for other in ("pos", "q", "k", "qr", "kr"):
+                if other == out:
+                    continue
+                for off in (0, 16, size[other] - 16, 16 - size[out]):
+                    if not (other == own and off == 0):
+                        assert call(**{out: at[other] + off}) == ARG, (out, other, off)
+        assert call(qr=at["k"], kr=at["q"]) == ARG and call(q=at["k"], qr=at["k"]) == ARG
+        if not torch.cuda.is_available():              # what is allowed gets as far as the device, of which there is none
+            for good in (call(), call(qr=at["q"]), call(kr=at["k"]), call(qr=at["q"], kr=at["k"]), call(q=at["k"]),
+                         call(qr=at["k"] + size["k"]), call(kr=at["q"] - size["kr"])):
+                assert good not in (0, ARG, SHAPE)

@@ -488,4 +488,9 @@ int bwd_split_override();                            // 0: automatic
 int fwd_split_override();                            // 0: automatic
 int plan_ok(const tree_plan_t* p);
 void record_timing_event(int i, cudaStream_t s);     // no-op unless events are registered
+// two buffers share a byte (NULL: none)
+inline bool buffers_meet(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + b_bytes && y < x + a_bytes;
+}
 }  // namespace ta

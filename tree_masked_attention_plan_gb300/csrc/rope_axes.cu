@@ -108,6 +108,12 @@ int rope_axes(const tree_plan_t* plan, const int32_t* pos, const int32_t* sectio
   AxesTable tab;
   const int half = d / 2;
   if (!axes_of(sections, n_axes, interleaved, half, tab.axis)) return TREE_ERR_SHAPE;
+  // A row is read before it is written, by the same lanes: an output may be its own input, but touch nothing else.
+  const size_t row = (size_t)plan->n_tokens * d * 2, nq = row * Hq, nk = row * Hkv, np = (size_t)plan->n_tokens * n_axes * 4;
+  if (buffers_meet(qr, nq, kr, nk) || buffers_meet(qr, nq, k, nk) || buffers_meet(kr, nk, q, nq) ||
+      buffers_meet(qr, nq, pos, np) || buffers_meet(kr, nk, pos, np) || (qr != q && buffers_meet(qr, nq, q, nq)) ||
+      (kr != k && buffers_meet(kr, nk, k, nk)))
+    return TREE_ERR_ARG;
   const double step = -std::log2(static_cast<double>(theta)) / half;
   for (int c = 0; c < half; ++c) {
     double f = std::exp2(step * c) * 0.15915494309189533577;          // turns per position

@@ -1775,10 +1775,7 @@ struct Buffer {
   bool tokens;
 };
 bool buffers_ok(const Buffer* out, int n_out, const Buffer* in, int n_in) {
-  auto meet = [](const Buffer& a, const Buffer& b) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return a.p && b.p && x < y + b.bytes && y < x + a.bytes;
-  };
+  auto meet = [](const Buffer& a, const Buffer& b) { return buffers_meet(a.p, a.bytes, b.p, b.bytes); };
   for (int i = 0; i < n_out; ++i) {
     for (int j = 0; j < i; ++j)
       if (meet(out[i], out[j])) return false;
