@@ -458,7 +458,8 @@ typedef struct {
   int32_t reserved;
 } tree_grad_t;
 
-/* Bytes of workspace (16-byte aligned, not initialised) for a list of n gradients. */
+/* Bytes of workspace (16-byte aligned, not initialised) for a list of n gradients.  It and the norm overlap
+ * no other buffer of a call (else TREE_ERR_ARG). */
 size_t tree_grad_workspace(int n);
 
 /* *norm (device fp32) = sqrt of the sum of squares of every element of the n >= 1 gradients (the

@@ -67,3 +67,25 @@ def test_rope_axes_buffers_that_overlap(lib):
             for good in (call(), call(qr=at["q"]), call(kr=at["k"]), call(qr=at["q"], kr=at["k"]), call(q=at["k"]),
                          call(qr=at["k"] + size["k"]), call(kr=at["q"] - size["kr"])):
                 assert good not in (0, ARG, SHAPE)
+
+
+def test_workspace_and_norm_that_overlap(lib):
+    """Neither lies in a gradient, a target or the other one."""
+    A, M = 1 << 30, 1 << 20
+    c = (tam.GradT * 3)()
+    for i, (numel, dtype) in enumerate(((1000, 0), (0, 1), (500, 1))):
+        c[i] = tam.GradT(A + 2 * i * M, A + (2 * i + 1) * M, numel, dtype, 0)
+    ws, norm, size = A + 10 * M, A + 11 * M, lib.tree_grad_workspace(3)
+    spots = [A, A + 1984, A + 4 * M, A + 4 * M + 1996]
+    targets = [p + M for p in spots]
+
+    def run(name, ws=ws, norm=norm):
+        return lib.tree_grad_norm(c, 3, ws, norm, None) if name == "norm" else lib.tree_grad_clip(c, 3, 1.0, ws, norm, None)
+
+    for name in ("norm", "clip"):
+        for p in spots + (targets if name == "clip" else []):
+            assert run(name, norm=p) == ARG and run(name, ws=p & ~15) == ARG and run(name, ws=(p & ~15) + 16 - size) == ARG
+        assert run(name, norm=ws) == ARG and run(name, norm=ws + size - 4) == ARG
+        if not torch.cuda.is_available():
+            for good in (run(name), run(name, norm=A + 2 * M), run(name, norm=ws + size), run(name, norm=A + 2000)):
+                assert good not in (0, ARG, SHAPE)

@@ -374,6 +374,19 @@ int all_squares(const tree_grad_t* list, int n, double* part, int* n_part, cudaS
 
 bool bad_ws(const void* p) { return !p || (reinterpret_cast<uintptr_t>(p) & 15); }
 
+// Partial sums and the norm are written while other blocks read gradients and write targets: they touch none, nor each other.
+bool results_apart(const tree_grad_t* list, int n, bool clip, const void* workspace, const float* norm) {
+  const size_t ws = tree_grad_workspace(n);
+  if (buffers_meet(workspace, ws, norm, 4)) return false;
+  for (int i = 0; i < n; ++i) {
+    const size_t b = (size_t)grad_bytes(list[i]);
+    if (!b) continue;
+    for (const void* p : {list[i].grad, clip ? static_cast<const void*>(list[i].out) : nullptr})
+      if (buffers_meet(p, b, workspace, ws) || buffers_meet(p, b, norm, 4)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace ta
 
@@ -390,6 +403,7 @@ int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
   int rc = check_list(list, n, false);
   if (rc) return rc;
   if (bad_ws(workspace) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return TREE_ERR_ARG;
+  if (!results_apart(list, n, false, workspace, norm)) return TREE_ERR_ARG;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -407,6 +421,7 @@ int tree_grad_clip(const tree_grad_t* list, int n, float max_norm, void* workspa
   if (rc) return rc;
   if (!(max_norm >= 0.f)) return TREE_ERR_SHAPE;
   if (bad_ws(workspace) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return TREE_ERR_ARG;
+  if (!results_apart(list, n, true, workspace, norm)) return TREE_ERR_ARG;
   rc = check_device();
   if (rc) return rc;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
