@@ -389,8 +389,8 @@ size_t tree_scan_workspace(const tree_plan_t* plan, int C);
  * gate, x, y: [N][C] in packed order, all of type dtype (TREE_BF16 or TREE_F32).
  * states: fp32 [tree_scan_rows()][C].  Row v < n_nodes receives node v's final state (zeros where the
  * node holds no tokens); the rows behind them are for the backward (row n_nodes + k: the state after
- * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout; y is rounded
- * once.  A state that becomes infinite or NaN stays so (either) along its paths and touches no
+ * token (k + 1) TREE_SCAN_TILE - 1, where there is one).  States are fp32 throughout, and so are
+ * decays: a token's may be off by 2^-25 (1 - a below that is lost); y is rounded once.  A state that becomes infinite or NaN stays so (either) along its paths and touches no
  * other path.
  * C a multiple of 8, at most 2^28 (else TREE_ERR_SHAPE); pointers 16-byte aligned (else TREE_ERR_ARG); the
  * workspace (tree_scan_workspace() bytes, 256-byte aligned, not initialised) belongs to one call at

@@ -1,0 +1,43 @@
+"""How near the operators come to their definition at values where fewer bits would show.  Rounding units are 2^-24."""
+import numpy as np
+import pytest
+import torch
+
+import tree_masked_attention_plan_gb300 as tam
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+F = torch.float32
+
+
+@pytest.mark.parametrize("n,tail", [(200, 0), (700, 0), (700, 300)])
+def test_the_weight_of_the_input_at_strong_sigmoid_gates(n, tail):
+    """One token a sequence, no state before it: y = (1 - a) x, and with x = 0 from a state of one y = a.  1 - a = e / (1 + e),
+    a = 1 / (1 + e), e = e^-g: the power 2^t is right to 2^-22 (4 units), what its argument lost is put back but for the
+    error of ln 2 in fp32 (0.05 units for each unit of g: 4.4 at 87) and one rounding; 1 + e and the reciprocal (2^-23)
+    take 1 + 2, two products 1: 13 units at most."""
+    C, lens = 8, [1] * n + [tail] * (tail > 0)         # (with the tail: the kernels for many tokens)
+    g = torch.linspace(-86.5, 86.5, n * C).reshape(n, C)
+    x = torch.rand(n, C, generator=torch.Generator().manual_seed(1)) + 1
+    plan, tree = tam.tree_plan([-1] * len(lens), lens, device=DEV), tam.tree_arrays([-1] * len(lens), lens, DEV)
+    long = lambda t: torch.cat([t, torch.zeros(tail, C)]).to(DEV)
+    y, _ = tam.tree_scan_fwd(plan, tree, long(g), long(x))
+    a, _ = tam.tree_scan_fwd(plan, tree, long(g), long(0 * x), init=torch.ones(len(lens), C, device=DEV))
+    gd = g.double().numpy()
+    for got, ref in ((y, x.double().numpy() / (1 + np.exp(gd))), (a, 1 / (1 + np.exp(-gd)))):
+        off = np.abs(got[:n].double().cpu().numpy() - ref) / ref * 2.0 ** 24
+        assert off.max() <= 13, (off.max(), gd.flat[off.argmax()])
+
+
+@pytest.mark.parametrize("rate", [1e-7, 2e-8, 1e-5])
+@pytest.mark.parametrize("n", [200, 5000])
+def test_decays_next_to_one(n, rate):
+    """A state of one that only decays, by 1 - a = `rate` a token: decay and step are rounded by 2^-25 each, where tiles are
+    joined a map's product and the sum behind it again (twice a tile of 128): 1.1 units of 2^-24 a token."""
+    C = 8
+    plan, tree = tam.tree_plan([-1], [n], device=DEV), tam.tree_arrays([-1], [n], DEV)
+    g = torch.full((n, C), -rate, device=DEV)
+    y, _ = tam.tree_scan_fwd(plan, tree, g, torch.zeros(n, C, device=DEV), init=torch.ones(1, C, device=DEV), gate_kind="log")
+    t = np.arange(1, n + 1)
+    off = np.abs(y.double().cpu().numpy() - np.exp(t * float(np.float32(-rate)))[:, None])
+    assert (off <= 1.1 * 2.0 ** -24 * t[:, None]).all()

@@ -29,9 +29,10 @@
 // Why 128 tokens: a tile hands on 4 bytes of state and 8 of map for each channel, and one of 64 tokens twice as
 // often (the tree: 0.53 instead of 0.42 ms forward, 1.00 instead of 0.78 backward).
 //
-// Precision: states, gates and gradients are fp32.  The forward holds a and 1 - a apart, each with the accuracy
-// of its own size.  The backward has one word for both: p = -(1 - a) where a > 1/2, p = a elsewhere, so
-// that neither the little that a long memory loses a token nor a small decay drowns in the other's rounding.
+// Precision: states, gates and gradients are fp32.  The forward holds a and the input's weight apart, each to the
+// accuracy that token_of states.  The backward has one word for both: p = -(1 - a) where a > 1/2, p = a elsewhere, so
+// that neither the little that a long memory loses a token nor a small decay drowns in the other's rounding; it computes
+// h again with that, from the forward's state before the tile, so that within a tile the two differ by roundings of a.
 #include <algorithm>
 #include <atomic>
 
@@ -287,7 +288,7 @@ DEVI float rcp_approx(float a) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
   return r;
 }
-// e^n for -100 <= n <= 0: 2^t of the hardware (2 units in the last place) at t = n log2(e) rounded, and the
+// e^n for -100 <= n <= 87: 2^t of the hardware (2 units in the last place) at t = n log2(e) rounded, and the
 // first-order term of what the rounding took from n
 template <int CH>
 DEVI Vec<CH> exp_of(Vec<CH> n) {
@@ -336,17 +337,29 @@ DEVI Vec<CH> gate_of(Vec<CH> g) {
 }
 
 // The forward's form of a token: decay a and input b.  Sigmoid: a = 1 / (1 + e) and 1 - a = e / (1 + e) with
-// e = e^-g, each with the relative accuracy of its own size; g is held above -87, where e is still finite and a
-// already below 2e-38.
-template <int KIND, int CH>
+// e = e^-g; g is held above -87, where e is still finite and a already below 2e-38.
+// fp32 tensors (EXACT): e as exp_of has it, so that a and 1 - a are right to 13 units of 2^-24 of their own size.  bf16
+// tensors: what the rounding of -g log2(e) takes is left out, 1 unit for each unit of |g| or so (17 at 16, 62 at 87): the
+// gate itself came with some 2^15 times as much.  With it one sequence of 32768 x 8192 takes 352 us instead of 338, the rollout
+// 398 instead of 388.
+// Log: b = x and a = 1 + p.  a is fp32 as the state is, so that a token may cost a state 2^-25 twice over, once in a and
+// once in a h + b: at memories of 2^20 tokens the rate is off by a thirtieth, and 1 - a below 2^-25 is lost.  p in its
+// place would not help: the product of decays that a map is made of is rounded in the same way.
+template <int KIND, bool EXACT, int CH>
 DEVI void token_of(Vec<CH> g, Vec<CH> x, Vec<CH>& a, Vec<CH>& b) {
   if (KIND == TREE_GATE_SIGMOID) {
     Vec<CH> n, e;
+    if (EXACT) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) n.v[c] = max_nan(g.v[c], -87.f);
-    n = n * vec<CH>(-1.4426950408889634f);
+      for (int c = 0; c < CH; ++c) n.v[c] = min_nan(max_nan(-g.v[c], -100.f), 87.f);
+      e = exp_of(n);
+    } else {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) e.v[c] = ex2_approx(n.v[c]);
+      for (int c = 0; c < CH; ++c) n.v[c] = max_nan(g.v[c], -87.f);
+      n = n * vec<CH>(-1.4426950408889634f);
+#pragma unroll
+      for (int c = 0; c < CH; ++c) e.v[c] = ex2_approx(n.v[c]);
+    }
     const Vec<CH> d = e + vec<CH>(1.f);
 #pragma unroll
     for (int c = 0; c < CH; ++c) a.v[c] = rcp_approx(d.v[c]);
@@ -920,7 +933,7 @@ DEVI void fwd_map(ScanShared& sh, uint8_t* slots, int warp, const WaitCtl& wc) {
 #pragma unroll 4
     for (int q = 0; q < kWarpTokens; ++q) {
       Vec<CH> a, b;
-      token_of<KIND>(rows.get(0, q), rows.get(1, q), a, b);
+      token_of<KIND, sizeof(T) == 4>(rows.get(0, q), rows.get(1, q), a, b);
       rows.set_token(q, a, b);
       B = vfma(a, B, b);
       A = A * a;
@@ -1633,7 +1646,7 @@ __global__ void __launch_bounds__(32 * kStepMost / kStepTokens) k_scan_step(cons
   for (int q = 0; q < kStepTokens; ++q) {
     if (t0 + q >= n) break;
     Vec<CH> d, b;
-    token_of<KIND>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
+    token_of<KIND, sizeof(T) == 4>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
     if ((roots >> q) & 1u) b = vfma(d, h0[q], b);
     sh_st(decay(t0 + q), d);
     sh_st(input(t0 + q), b);
@@ -1703,7 +1716,7 @@ __global__ void __launch_bounds__(32 * kStepMost / kStepTokens) k_scan_step(cons
     for (int q = 0; q < kStepTokens; ++q) {
       if (at + q >= end) break;
       Vec<CH> d, b;
-      token_of<KIND>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
+      token_of<KIND, sizeof(T) == 4>(Lane<T>::unpack(gw[q]), Lane<T>::unpack(xw[q]), d, b);
       h = vfma(d, h, b);
       if (on) *reinterpret_cast<uint32_t*>(a.y + (size_t)(base + at + q) * a.C + ch) = Lane<T>::pack(h);
       if (on && at + q == end - 1) st_state(a.states + (size_t)v * a.C + ch, h);
