@@ -470,10 +470,11 @@ int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
                    tree_stream_t stream);
 
 /* The norm as tree_grad_norm, and out = grad * (max_norm / norm) where max_norm < norm, else (also
- * for an infinite or NaN norm: read it, and skip the step) out = grad.  max_norm >= 0, may be
+ * for an infinite or NaN norm: read it, and skip the step) out = grad.  The quotient is taken in fp64 and
+ * rounded to fp32 once.  max_norm >= 0, may be
  * infinite (else TREE_ERR_SHAPE).  An `out` that overlaps another gradient or `out`, or its own
  * gradient other than as a whole, is refused (TREE_ERR_ARG), a gradient listed twice in place too. */
-int tree_grad_clip(const tree_grad_t* list, int n, float max_norm, void* workspace, float* norm,
+int tree_grad_clip(const tree_grad_t* list, int n, double max_norm, void* workspace, float* norm,
                    tree_stream_t stream);
 
 /* ---------------------------------------------------------------------------------------
@@ -525,6 +526,7 @@ int tree_set_timing_events(void* const* events, int n);
 
 const char* tree_strerror(int code);
 const char* tree_last_cuda_error(void);
+/* 2: the plan structs end with the longest node, tree_grad_clip takes max_norm as double. */
 int tree_version(void);
 
 #ifdef __cplusplus

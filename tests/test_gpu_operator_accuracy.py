@@ -41,3 +41,15 @@ def test_decays_next_to_one(n, rate):
     t = np.arange(1, n + 1)
     off = np.abs(y.double().cpu().numpy() - np.exp(t * float(np.float32(-rate)))[:, None])
     assert (off <= 1.1 * 2.0 ** -24 * t[:, None]).all()
+
+
+@pytest.mark.parametrize("n", [3, 5, 50000])
+def test_the_coefficient_of_clipping(n):
+    """max_norm is taken as it is given: the coefficient max_norm / norm is rounded once, half a step of fp32, one unit at
+    most.  Equal elements of 2 have exact squares and sums, and their product with the coefficient is exact."""
+    for max_norm in np.random.default_rng(n).uniform(0.1, 0.9, 40):
+        grads = [torch.full((n,), 2.0, device=DEV)]
+        norm = 2.0 * np.sqrt(np.float64(n))
+        tam.tree_grad_clip(grads, float(max_norm))
+        off = abs(grads[0][0].item() / (2.0 * max_norm / norm) - 1) * 2.0 ** 24
+        assert off <= 1 + 1e-6 and (grads[0] == grads[0][0]).all(), (max_norm, off)

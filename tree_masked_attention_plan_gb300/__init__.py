@@ -127,7 +127,7 @@ def _lib():
                                  _vp, _vp, _vp]),
         "tree_grad_workspace": (ctypes.c_size_t, [_i32]),
         "tree_grad_norm": (_i32, [_vp, _i32, _vp, _vp, _vp]),
-        "tree_grad_clip": (_i32, [_vp, _i32, _f32, _vp, _vp, _vp]),
+        "tree_grad_clip": (_i32, [_vp, _i32, ctypes.c_double, _vp, _vp, _vp]),
         "tree_ce_workspace": (ctypes.c_size_t, [P(PlanT), _i32, _i32, _i32]),
         "tree_ce_fwd_bwd": (_i32, [P(PlanT), _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _vp]),

@@ -263,13 +263,13 @@ DEVI void chunk_out(const uint8_t* p, uint8_t* o, int64_t n, bool clip, float c)
 // last ones first: they are the ones that the norm's pass left in L2.
 template <int MAX>
 __global__ void __launch_bounds__(kGradThreads) k_grad_scale(const __grid_constant__ GradList<MAX> L,
-                                                             const double* part, int n_part, float max_norm,
+                                                             const double* part, int n_part, double max_norm,
                                                              float* norm) {
   __shared__ double red[kGradThreads / 32];
   const double total = sqrt(total_squares(part, n_part, red));
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = static_cast<float>(total);
-  const bool clip = total > (double)max_norm && (float)total < INFINITY;      // false for NaN
-  const float coef = clip ? static_cast<float>((double)max_norm / total) : 1.f;
+  const bool clip = total > max_norm && (float)total < INFINITY;      // false for NaN
+  const float coef = clip ? static_cast<float>(max_norm / total) : 1.f;
   for (int c = L.chunks - 1 - blockIdx.x; c >= 0; c -= gridDim.x) {
     const GradEntry& e = L.e[entry_of(L, c)];
     const int64_t at = (int64_t)(c - e.first) * kChunk;
@@ -349,7 +349,7 @@ int squares_of(const tree_grad_t* list, int n, double* part, int* blocks, cudaSt
 }
 
 template <int MAX>
-int scale_by(const tree_grad_t* list, int n, const double* part, int n_part, float max_norm, float* norm,
+int scale_by(const tree_grad_t* list, int n, const double* part, int n_part, double max_norm, float* norm,
              cudaStream_t s) {
   GradList<MAX> L;
   fill(&L, list, n);
@@ -415,11 +415,11 @@ int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
   return record_cuda(cudaGetLastError());
 }
 
-int tree_grad_clip(const tree_grad_t* list, int n, float max_norm, void* workspace, float* norm,
+int tree_grad_clip(const tree_grad_t* list, int n, double max_norm, void* workspace, float* norm,
                    tree_stream_t stream) {
   int rc = check_list(list, n, true);
   if (rc) return rc;
-  if (!(max_norm >= 0.f)) return TREE_ERR_SHAPE;
+  if (!(max_norm >= 0.0)) return TREE_ERR_SHAPE;
   if (bad_ws(workspace) || !norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return TREE_ERR_ARG;
   if (!results_apart(list, n, true, workspace, norm)) return TREE_ERR_ARG;
   rc = check_device();

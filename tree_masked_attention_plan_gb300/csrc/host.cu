@@ -237,6 +237,6 @@ const char* tree_strerror(int code) {
 
 const char* tree_last_cuda_error(void) { return g_last_err; }
 
-int tree_version(void) { return 1; }
+int tree_version(void) { return 2; }
 
 }  // extern "C"
