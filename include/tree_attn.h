@@ -182,7 +182,7 @@ int tree_apply_weights(const tree_plan_t* plan, const tree_bf16* u, tree_bf16* d
  * has i, i + n_axes, i + 2 n_axes, ... until it has its share (all of them below d/2), and axis 0
  * what is left.  Rotate-half pairs and layouts as tree_rope_fwd; in place allowed (qr = q, kr = k),
  * no other overlap of an output with another buffer (TREE_ERR_ARG).  The angle is
- * exact to 2^-24 turns at every position.  One axis with pos = the plan's `pos` is
+ * exact to 2^-25 turns at every position (theta >= 2^-40; below, only near position 0).  One axis with pos = the plan's `pos` is
  * tree_rope_fwd with more exact angles.  n_axes outside 1..TREE_MAX_AXES, sections that do not
  * describe d/2 frequencies, d not 64/128, bad heads or theta -> TREE_ERR_SHAPE. */
 int tree_rope_axes_fwd(const tree_plan_t* plan, const int32_t* pos, const int32_t* sections,

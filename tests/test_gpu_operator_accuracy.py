@@ -1,4 +1,6 @@
 """How near the operators come to their definition at values where fewer bits would show.  Rounding units are 2^-24."""
+from decimal import Decimal, getcontext
+
 import numpy as np
 import pytest
 import torch
@@ -7,7 +9,6 @@ import tree_masked_attention_plan_gb300 as tam
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
-F = torch.float32
 
 
 @pytest.mark.parametrize("n,tail", [(200, 0), (700, 0), (700, 300)])
@@ -53,3 +54,32 @@ def test_the_coefficient_of_clipping(n):
         tam.tree_grad_clip(grads, float(max_norm))
         off = abs(grads[0][0].item() / (2.0 * max_norm / norm) - 1) * 2.0 ** 24
         assert off <= 1 + 1e-6 and (grads[0] == grads[0][0]).all(), (max_norm, off)
+
+
+@pytest.mark.parametrize("theta", [1.0, 1.25, 2.0, 10000.0, 1e12, 0.5, 0.01, 1e-4, 2.0 ** -40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_angles_at_the_ends_of_the_positions(theta, d):
+    """The rotation of a pair (1, 0) is (cos, sin) of its angle, which is right to 2^-25 turns at every position for every
+    theta of 2^-40 and more; sine and cosine add 2 units of 2^-24, the result is rounded to bf16, half a step.  Most of the
+    4000 positions are far out, so that some cosines and sines lie at zero and at borders of rounding, where the angle shows."""
+    half = d // 2
+    ps = [0, 1, -1, 12345, 2 ** 31 - 1, -2 ** 31, 2 ** 30 + 1, 2 ** 31 - 54321]
+    ps += [int(v) for v in np.random.default_rng(d).integers(-2 ** 31, 2 ** 31, 4000)]
+    N = len(ps)
+    q = torch.zeros(N, 1, d, dtype=torch.bfloat16, device=DEV)
+    q[..., :half] = 1
+    plan = tam.tree_plan([-1], [N], device=DEV)
+    pos = torch.tensor([ps], dtype=torch.int64).to(torch.int32).to(DEV)
+    out, _ = tam.tree_rope_axes_fwd(plan, pos, q, q.clone(), (half,), theta=theta)
+    out = out[:, 0].double().cpu().numpy()
+    # turns of position and frequency, modulo one, in whole numbers: frequencies as fractions of 2^160
+    getcontext().prec = 90
+    th, pi = Decimal(float(np.float32(theta))), Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    turn = np.empty((N, half))
+    for c in range(half):
+        f = int((-th.ln() * c / half).exp() / (2 * pi) * 2 ** 160)
+        turn[:, c] = [((p * f) % 2 ** 160) / 2 ** 160 for p in ps]
+    ang = 2 * np.pi * turn
+    for got, ref in ((out[:, :half], np.cos(ang)), (out[:, half:], np.sin(ang))):
+        tol = 2.0 ** -8 * np.abs(ref) + 2 * np.pi * 2.0 ** -25 + 2.0 ** -23
+        assert (np.abs(got - ref) <= tol).all()

@@ -5,8 +5,9 @@
 //   a = pos[axis(c)][t] * theta^(-2c/d);   the gradient goes through the rotation by -a.
 // Angles are exact to fp32 at any int32 position: a frequency is held as a 64-bit fraction of a
 // turn, so that pos * frequency wraps modulo one turn by itself in integer arithmetic, and only
-// the wrapped fraction becomes a float (error 2^-25 turns, where pos * frequency in fp32 loses
-// whole radians beyond position 10^6).
+// the wrapped fraction becomes a float (error 2^-26 turns, where pos * frequency in fp32 loses
+// whole radians beyond position 10^6).  The table is made in pairs of doubles: in doubles alone its frequencies were
+// off by up to 2^-55, 2^-24 turns at position 2^31, and for theta < 1, where they are many turns, by far more.
 // HBM-bound: every head of q and k is read and written once.  32768 tokens of 40 heads of 128: 104 us, 6.4 TB/s;
 // the gradient of 9973 tokens of 32 heads of 64: 16.5 us, 5.0 TB/s (82 MB, of which much stays in L2).
 #include <cmath>
@@ -67,6 +68,43 @@ __global__ void __launch_bounds__(kAxesThreads) k_rope_axes(const __grid_constan
   }
 }
 
+// A number as the sum of two doubles, about 106 bits.  Dekker's and Knuth's error-free sums, products through fma.
+struct Pair {
+  double hi, lo;
+};
+Pair pair_of(double a, double b) {                   // |a| >= |b|
+  const double s = a + b;
+  return {s, b - (s - a)};
+}
+Pair times(Pair a, Pair b) {
+  const double p = a.hi * b.hi, e = std::fma(a.hi, b.hi, -p);
+  return pair_of(p, e + std::fma(a.hi, b.lo, a.lo * b.hi));
+}
+Pair root(Pair a) {                                  // one Newton step from the double's root
+  const double s = std::sqrt(a.hi), d = std::fma(-s, s, a.hi) + a.lo;
+  return pair_of(s, d / (2.0 * s));
+}
+Pair inverse(Pair a) {
+  const double q = 1.0 / a.hi, r = std::fma(-q, a.hi, 1.0) - q * a.lo;
+  return pair_of(q, q * r);
+}
+// theta^(-c / half) / (2 pi) turns for c < half, as fractions of 2^64; half is a power of two.  The powers of one root
+// (two chains, each other's latency): their error grows to some 2^-97 of their size; whole turns (theta < 1) drop out.
+void turns_of(double theta, int half, uint64_t* turn) {
+  Pair r{theta, 0.0};
+  for (int h = half; h > 1; h /= 2) r = root(r);
+  r = inverse(r);
+  const Pair start{0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};        // 1 / (2 pi)
+  Pair f[2] = {start, times(start, r)};
+  r = times(r, r);
+  for (int c = 0; c < half; ++c) {
+    Pair& g = f[c & 1];
+    const double hi = g.hi - std::floor(g.hi), lo = g.lo - std::floor(g.lo + 0.5);       // [0, 1), [-1/2, 1/2)
+    turn[c] = static_cast<uint64_t>(hi * 0x1p64) + static_cast<uint64_t>(static_cast<int64_t>(lo * 0x1p64));
+    g = times(g, r);
+  }
+}
+
 // The axis of every frequency.  In runs: the first sections[0] frequencies on axis 0, and so on.
 // Interleaved: axis i >= 1 takes frequencies i, i + n, i + 2n, ... until it has sections[i] of
 // them; the rest belongs to axis 0.  False where the sections do not describe d/2 frequencies.
@@ -114,12 +152,7 @@ int rope_axes(const tree_plan_t* plan, const int32_t* pos, const int32_t* sectio
       buffers_meet(qr, nq, pos, np) || buffers_meet(kr, nk, pos, np) || (qr != q && buffers_meet(qr, nq, q, nq)) ||
       (kr != k && buffers_meet(kr, nk, k, nk)))
     return TREE_ERR_ARG;
-  const double step = -std::log2(static_cast<double>(theta)) / half;
-  for (int c = 0; c < half; ++c) {
-    double f = std::exp2(step * c) * 0.15915494309189533577;          // turns per position
-    f -= std::floor(f);                                               // theta < 1: whole turns drop out
-    tab.turn[c] = static_cast<uint64_t>(std::ldexp(f, 64));           // f < 1; 53 bits: exact
-  }
+  turns_of(theta, half, tab.turn);
   rc = check_device();
   if (rc) return rc;
   const int N = plan->n_tokens;
