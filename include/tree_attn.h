@@ -463,8 +463,9 @@ typedef struct {
 size_t tree_grad_workspace(int n);
 
 /* *norm (device fp32) = sqrt of the sum of squares of every element of the n >= 1 gradients (the
- * list is host memory, free when the call returns).  The sum is held in pairs of fp32 and in fp64; the
- * norm is right wherever it is an fp32 number, also where the squares are not.  Infinite or NaN elements give such a norm.
+ * list is host memory, free when the call returns).  16 bytes of elements are squared and summed in fp32,
+ * these sums in pairs of fp32 and in fp64: the norm is right to 8 units of 2^-24 wherever it is an fp32
+ * number, also where the squares are not.  Infinite or NaN elements give such a norm.
  * Deterministic. */
 int tree_grad_norm(const tree_grad_t* list, int n, void* workspace, float* norm,
                    tree_stream_t stream);

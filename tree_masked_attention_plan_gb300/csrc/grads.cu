@@ -44,6 +44,8 @@ struct GradList {
 // vector made the norm of 528M fp32 elements take 2.4 ms instead of 0.3), so a vector's squares are summed in
 // fp32 and the vectors' sums in a pair of fp32 that holds what each addition rounds away.  A vector with a value
 // above 2^40 or with none above 2^-50, whose squares fp32 may not hold, is squared and summed in fp64.
+// A vector's sum takes 4 roundings (fp32) or 7 (bf16, whose squares are exact), the pair by the time that it holds as many
+// equal values as fit the memory 7 more: 7 units of 2^-24 in the norm, and its own rounding.
 struct Squares {
   float s = 0.f, c = 0.f;
   double rest = 0.0;

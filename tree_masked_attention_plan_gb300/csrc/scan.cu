@@ -23,8 +23,9 @@
 // 0.34 ms, 4.8 TB/s, backward 0.57 ms, 4.7 TB/s; a tree of the same size (nodes of some 250 tokens) 0.39 and
 // 0.70 ms.  What bounds it there is instruction issue and the dependent steps of a warp's walk (in the backward a
 // step of 64 channels takes 109 instructions, and the SM issues in 62 % of all cycles; the copies alone, without
-// the arithmetic, take 0.27 ms in the forward).  In a tree of short nodes or of few channels it is the way of a
-// state through the tiles, one after the other: 3456 tokens of a caterpillar by 4096 channels take 95 us, 13 at the
+// the arithmetic, take 0.27 ms in the forward).  In a tree of short nodes it is the way of a state through tiles in
+// which a break starts from a node that ends there too: they hand on a state, warp by warp, 3.5 us a tile (a tile
+// without breaks hands on its map: 0.4).  3456 tokens of a caterpillar by 4096 channels take 95 us, 13 at the
 // memory's rate.
 // Why 128 tokens: a tile hands on 4 bytes of state and 8 of map for each channel, and one of 64 tokens twice as
 // often (the tree: 0.53 instead of 0.42 ms forward, 1.00 instead of 0.78 backward).
